@@ -15,7 +15,7 @@ import re
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB_PATH = os.path.join(HERE, "libec.so")
-HEADERS = [os.path.join(ROOT, "include", h) for h in ("ec.h", "ec_huffman.h")]
+HEADERS = [os.path.join(ROOT, "include", h) for h in ("ec.h", "ec_huffman.h", "ec_mx.h", "ec_experts.h")]
 
 EC_OK, EC_ERR_INVALID, EC_ERR_CAPACITY, EC_ERR_CORRUPT = 0, 1, 2, 3
 EC_ERR_DEVICE, EC_ERR_OOM, EC_ERR_UNSUPPORTED = 4, 5, 6
@@ -122,6 +122,30 @@ def lib():
     L.ec_huff_encode_segments.argtypes = [vp, ctypes.c_uint32, u64, vp, vp, vp, u64, vp, sz, vp]
     L.ec_huff_decode_segments.restype = st
     L.ec_huff_decode_segments.argtypes = [vp, vp, vp, u64, ctypes.c_uint32, u64, vp, vp, sz, vp]
+    u32, i = ctypes.c_uint32, ctypes.c_int
+    for name, result, args in (
+        ("ec_mx_padded", u64, (u64,)),
+        ("ec_mx_padded_groups", u64, (u64, u32)),
+        ("ec_mx_quantize", st, (vp, i, u64, u64, u64, vp, vp, vp)),
+        ("ec_mx_quantize_both", st, (vp, i, u64, u64, u64, u64, u64, vp, vp, vp, vp, vp)),
+        ("ec_mx_quantize_groups", st, (vp, i, u64, u64, u64, vp, u32, vp, vp, vp, vp, vp)),
+        ("ec_mx_dequantize", st, (vp, vp, u64, u64, vp, i, u64, vp)),
+        ("ec_mx_product", st, (vp, vp, u64, vp, vp, u64, u64, vp, i, vp)),
+        ("ec_mx_product_experts", st, (vp, vp, u64, vp, vp, u64, u64, vp, u32, vp, i, vp)),
+        ("ec_mx_product_tokens", st, (vp, vp, u64, vp, vp, u64, u64, vp, u32, vp, i, vp)),
+        ("ec_mx_linear_workspace_bytes", sz, (u64, u64, u64, u32)),
+        ("ec_mx_linear", st, (vp, i, u64, u64, u64, vp, vp, u64, vp, u32, vp, vp, sz, vp)),
+        ("ec_expert_sort_workspace_bytes", sz, (u64, u32)),
+        ("ec_expert_sort", st, (vp, u32, u64, u32, vp, vp, vp, vp, sz, vp)),
+        ("ec_expert_dispatch", st, (vp, i, u64, u64, vp, u32, vp, u32, vp, vp)),
+        ("ec_expert_dispatch_mx", st, (vp, i, u64, u64, vp, u32, vp, u32, vp, vp, vp)),
+        ("ec_expert_dispatch_backward", st, (vp, i, u64, u64, vp, u32, vp, vp)),
+        ("ec_expert_combine", st, (vp, i, u64, u64, vp, u32, vp, i, vp, vp)),
+        ("ec_expert_combine_backward", st,
+         (vp, vp, i, u64, u64, vp, u32, vp, i, vp, u32, vp, vp, vp)),
+    ):
+        f = getattr(L, name)
+        f.restype, f.argtypes = result, list(args)
     _lib = L
     return L
 
@@ -497,3 +521,24 @@ class Huffman:
     def status(self, stream=None) -> int:
         """Wait for the stream; status of the last call on this workspace."""
         return int(lib().ec_huff_status(self._work, _stream_handle(stream)))
+
+
+# --- the 4-bit format and the token exchange (include/ec_mx.h, ec_experts.h) -
+_OPERATORS = {
+    "mx": ("MXTensor", "MXLinearSaved", "mx_quantize", "mx_quantize_both", "mx_dequantize",
+           "mx_product", "mx_linear", "mx_experts_linear", "mx_linear_forward",
+           "mx_linear_backward", "mx_experts_forward", "mx_experts_backward"),
+    "experts": ("Routing", "expert_sort", "expert_dispatch", "expert_dispatch_mx",
+                "expert_dispatch_backward", "expert_combine", "expert_combine_backward"),
+}
+
+
+def __getattr__(name):
+    # these modules import torch, which the rest of the binding leaves to its calls
+    import importlib
+    for module, names in _OPERATORS.items():
+        if name in names:
+            value = getattr(importlib.import_module(f"{__name__}.{module}"), name)
+            globals()[name] = value
+            return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

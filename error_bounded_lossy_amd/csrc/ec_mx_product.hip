@@ -1,0 +1,688 @@
+// Products of operands in the microscaled 4-bit format (include/ec_mx.h) on
+// the matrix cores' scaled instructions: y = a b^T with both operands stored
+// along the contraction, blocks of 32 sharing a scale.
+#include "ec_mx_device.h"
+
+using namespace ecmx;
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kFp4 = 4;  // the instructions' code of the element type
+
+enum { kDense = 0, kExperts = 1, kTokens = 2 };
+
+struct Operand {
+  const uint8_t* codes;
+  const uint8_t* scales;
+};
+
+struct Product {
+  Operand a, b;
+  void* y;
+  const int32_t* offsets;
+  uint64_t rows;     // of y (kExperts: of all groups; kTokens: of one expert's y)
+  uint32_t cols;     // of y
+  uint32_t depth;    // elements of a stored row
+  uint32_t experts;
+  uint32_t m_tiles, n_tiles;
+  uint64_t tokens;   // kTokens: rows that the groups divide
+};
+
+// ---------------------------------------------------------------- tiles
+
+// One workgroup of 2 by WN waves computes a tile of 64 FM rows by 32 FN WN
+// columns, a wave 32 FM by 32 FN of it with 32x32x64 instructions, whose rate
+// measured 8.6 PFLOP/s against 6.8 of the 16x16x128 ones.
+//
+// A stage is 128 elements (64 bytes) of every row of both operands plus their
+// 4 scale bytes, brought to LDS without passing registers.  Four stages are in
+// LDS: one is multiplied while the loads of the next three fly, with one
+// barrier a stage, placed before the last multiplications so that they cover
+// the first reads of the next stage.
+//
+// The order within the contraction is free as long as both operands agree, so
+// lane group g of instruction step s takes the 16-byte chunk 2 g + s of a
+// row: a lane's two scale bytes of a stage are then one half word, and the
+// step selects its byte in the instruction.  Chunks are stored at their number
+// xor bits 1 and 2 of the row, so that 8 lanes of consecutive rows read 8
+// different 16-byte columns of 128.
+template <int BM, int BN>
+struct Stage {
+  uint8_t a[BM * 64];
+  uint8_t b[BN * 64];
+  uint8_t s[(BM + BN) * 4];  // scales of a, then of b
+};
+
+__device__ __forceinline__ void to_lds16(const uint8_t* from, uint8_t* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+__device__ __forceinline__ void to_lds4(const uint8_t* from, uint8_t* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)to, 4, 0, 0);
+}
+
+__device__ __forceinline__ i32x8 widened(const i32x4& v) {
+  return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};  // 4-bit operands use half
+}
+
+template <int FM, int FN>
+struct Fragments {
+  i32x4 a[FM], b[FN];
+};
+template <int FM, int FN>
+struct Scales {
+  int a[FM], b[FN];
+};
+
+// Where this lane reads in a stage.
+struct Lane {
+  uint32_t a, b, sa, sb;  // step 0's chunk of its first rows; its scales
+};
+
+template <int BM, int BN, int FM, int FN>
+__device__ __forceinline__ void read(const Stage<BM, BN>& st, const Lane& at, int step,
+                                     Fragments<FM, FN>& f) {
+  // chunk 2 g + 1 lies at the place of chunk 2 g with the lowest bit turned
+#pragma unroll
+  for (int i = 0; i < FN; i++)
+    f.b[i] = *reinterpret_cast<const i32x4*>(st.b + (at.b ^ (step << 4)) + i * 2048);
+#pragma unroll
+  for (int i = 0; i < FM; i++)
+    f.a[i] = *reinterpret_cast<const i32x4*>(st.a + (at.a ^ (step << 4)) + i * 2048);
+}
+template <int BM, int BN, int FM, int FN>
+__device__ __forceinline__ void read(const Stage<BM, BN>& st, const Lane& at, Scales<FM, FN>& f) {
+#pragma unroll
+  for (int i = 0; i < FM; i++)
+    f.a[i] = *reinterpret_cast<const uint16_t*>(st.s + at.sa + i * 128);
+#pragma unroll
+  for (int i = 0; i < FN; i++)
+    f.b[i] = *reinterpret_cast<const uint16_t*>(st.s + at.sb + i * 128);
+}
+
+template <int FM, int FN, int STEP>
+__device__ __forceinline__ void multiply(const Fragments<FM, FN>& f, const Scales<FM, FN>& s,
+                                         f32x16 (&acc)[FM][FN]) {
+#pragma unroll
+  for (int i = 0; i < FM; i++)
+#pragma unroll
+    for (int j = 0; j < FN; j++)
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          widened(f.b[j]), widened(f.a[i]), acc[i][j], kFp4, kFp4, STEP, s.b[j], STEP, s.a[i]);
+}
+
+// Waits until at most N of this wave's loads are under way and its LDS reads
+// have returned, then for the other waves.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  static_assert(N < 64, "the counter's range");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Tiles in the order that keeps the L2 caches useful: consecutive workgroups
+// go to the 8 XCDs in turn, so each XCD takes a run of consecutive tiles; in a
+// run, 8 tiles along the rows share a column tile.
+__device__ __forceinline__ bool tile_of(uint32_t tiles, uint32_t& t) {
+  const uint32_t run = (tiles + 7) / 8;
+  t = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
+  return (blockIdx.x >> 3) < run && t < tiles;
+}
+
+template <int FM, int FN, int WN, typename T, int MODE>
+__global__ __launch_bounds__(128 * WN, 2) void mx_tiles(const Product p) {
+  constexpr int BM = 64 * FM, BN = 32 * FN * WN, kWaves = 2 * WN;
+  using St = Stage<BM, BN>;
+  constexpr uint32_t kShift = FM == 1 ? 6 : FM == 2 ? 7 : 8;
+  static_assert((1u << kShift) == BM, "tile rows");
+  // four variables, not an array: the compiler then knows which loads a read waits for
+  __shared__ __attribute__((aligned(16))) St st0, st1, st2, st3;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const uint32_t wm = wave & 1, wn = wave >> 1;
+
+  uint32_t t;
+  if (!tile_of(p.m_tiles * p.n_tiles * (MODE == kTokens ? p.experts : 1), t)) return;
+  uint32_t e = 0;
+  if (MODE == kTokens) {
+    e = t / (p.m_tiles * p.n_tiles);
+    t -= e * (p.m_tiles * p.n_tiles);
+  }
+  const uint32_t width = 8 * p.n_tiles, band = t / width;
+  const uint32_t high = min(p.m_tiles - band * 8, 8u);
+  uint32_t tm = band * 8 + (t - band * width) % high;
+  const uint32_t tn = (t - band * width) / high;
+
+  // this tile's rows [m0, m_end) of a and y, its columns, its contraction
+  uint64_t m0 = (uint64_t)tm * BM, m_end = p.rows;
+  const uint32_t n0 = tn * BN;
+  uint64_t k0 = 0;        // first element of the contraction in a stored row
+  uint32_t k_len = p.depth;
+  T* y = (T*)p.y;
+  const uint8_t *bc = p.b.codes, *bs = p.b.scales;
+  if (MODE == kExperts) {
+    const GroupTile gt = find_tile(p.offsets, p.experts, p.rows, kShift, tm);
+    if (gt.group == p.experts) {  // rows of no group: zeros
+      int64_t first = p.offsets[p.experts];
+      first = first < 0 ? 0 : first;
+      m0 = (uint64_t)first + (uint64_t)gt.local * BM;
+      const uint64_t end = min(m0 + BM, p.rows);
+      for (uint64_t r = m0 + wave; r < end; r += kWaves)
+        for (uint32_t c = n0 + lane; c < min(n0 + (uint32_t)BN, p.cols); c += 64)
+          y[r * p.cols + c] = (T)0.0f;
+      return;
+    }
+    m0 = gt.first + (uint64_t)gt.local * BM;
+    m_end = gt.first + gt.count;
+    bc += (uint64_t)gt.group * p.cols * (p.depth / 2);
+    bs += (uint64_t)gt.group * p.cols * (p.depth / 32);
+  }
+  if (MODE == kTokens) {
+    uint64_t first, count;
+    group_rows(p.offsets, e, p.tokens, first, count);
+    k0 = (uint64_t)group_start(p.offsets, e, p.tokens) * 128;
+    k_len = (uint32_t)((count + 127) / 128 * 128);
+    if (k0 >= p.depth) k_len = 0;  // only with offsets out of order
+    else if (k0 + k_len > p.depth) k_len = p.depth - (uint32_t)k0;
+    if (k_len == 0) k0 = 0;
+    y += (uint64_t)e * p.rows * p.cols;
+  }
+
+  // What this lane loads: of instruction q of an operand, row 16 q + lane / 4
+  // and chunk (lane & 3) xor bits 1 and 2 of the row.  Rows past the end read
+  // the last one: they only reach results that are not stored.
+  const uint32_t pitch = p.depth / 2, spitch = p.depth / 32;
+  const uint32_t m_last = (uint32_t)(m_end - m0) - 1, n_last = p.cols - n0 - 1;
+  const uint8_t* ga = p.a.codes + m0 * pitch + k0 / 2;
+  const uint8_t* gsa = p.a.scales + m0 * spitch + k0 / 32;
+  const uint8_t* gb = bc + (uint64_t)n0 * pitch + k0 / 2;
+  const uint8_t* gsb = bs + (uint64_t)n0 * spitch + k0 / 32;
+  const uint32_t chunk = (lane & 3) ^ ((lane >> 3) & 3);
+  // offsets from the tile's first row: at most 256 rows of 2^23 bytes
+  constexpr int LA = BM / 16 / kWaves, LB = BN / 16 / kWaves;  // a wave's loads of a stage
+  uint32_t oa[LA], ob[LB];
+#pragma unroll
+  for (int i = 0; i < LA; i++)
+    oa[i] = min((wave * LA + i) * 16 + (lane >> 2), m_last) * pitch + chunk * 16;
+#pragma unroll
+  for (int i = 0; i < LB; i++)
+    ob[i] = min((wave * LB + i) * 16 + (lane >> 2), n_last) * pitch + chunk * 16;
+  // scales: 64 rows an instruction; every wave loads the same number of times,
+  // some of them what another one loads too, so that all count alike
+  constexpr int SA = BM / 64, SN = (BM + BN) / 64;  // of a, of both
+  constexpr int kScaleLoads = (SN + kWaves - 1) / kWaves, kLoads = LA + LB + kScaleLoads;
+  const uint8_t* gs[kScaleLoads];
+  uint32_t os[kScaleLoads], ls[kScaleLoads];
+#pragma unroll
+  for (int i = 0; i < kScaleLoads; i++) {
+    const uint32_t q = (wave + kWaves * i) % SN;
+    const bool is_a = q < SA;
+    gs[i] = is_a ? gsa : gsb;
+    os[i] = min((is_a ? q : q - SA) * 64 + lane, is_a ? m_last : n_last) * spitch;
+    ls[i] = q * 256;
+  }
+  const uint32_t stages = __builtin_amdgcn_readfirstlane(k_len / 128);
+  // Past the last stage it is loaded again, so that every turn below does the
+  // same and waits for the same number of loads.
+  auto load = [&](St& st, uint32_t stage) {
+    uint32_t c = __builtin_amdgcn_readfirstlane(min(stage, stages - 1));
+    // kept a scalar: the compiler would otherwise carry an address per load and lane
+    asm volatile("" : "+s"(c));
+#pragma unroll
+    for (int i = 0; i < LA; i++) to_lds16(ga + c * 64 + oa[i], st.a + (wave * LA + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < LB; i++) to_lds16(gb + c * 64 + ob[i], st.b + (wave * LB + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; i++) to_lds4(gs[i] + c * 4 + os[i], st.s + ls[i]);
+  };
+
+  const uint32_t r = lane & 31, g = lane >> 5;
+  Lane at;
+  at.a = (wm * 32 * FM + r) * 64 + ((2 * g) ^ ((r >> 1) & 3)) * 16;
+  at.b = (wn * 32 * FN + r) * 64 + ((2 * g) ^ ((r >> 1) & 3)) * 16;
+  at.sa = (wm * 32 * FM + r) * 4 + g * 2;
+  at.sb = (BM + wn * 32 * FN + r) * 4 + g * 2;
+
+  f32x16 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; i++)
+#pragma unroll
+    for (int j = 0; j < FN; j++) acc[i][j] = f32x16{};
+
+  if (stages > 0) {
+    load(st0, 0);
+    load(st1, 1);
+    load(st2, 2);
+    wait_and_meet<2 * kLoads>();
+    Fragments<FM, FN> f0, f1;
+    Scales<FM, FN> sc;
+    read(st0, at, sc);
+    read(st0, at, 0, f0);
+    // Stage s is in `now`; its first fragments and scales are in registers.
+    auto turn = [&](uint32_t s, const St& now, const St& next,
+                    St& free) {
+      load(free, s + 3);
+      read(now, at, 1, f1);
+      multiply<FM, FN, 0>(f0, sc, acc);
+      wait_and_meet<2 * kLoads>();
+      Scales<FM, FN> snext;
+      read(next, at, snext);
+      read(next, at, 0, f0);
+      multiply<FM, FN, 1>(f1, sc, acc);
+      sc = snext;
+    };
+    for (uint32_t s = 0;; s += 4) {
+      turn(s, st0, st1, st3);
+      if (s + 1 >= stages) break;
+      turn(s + 1, st1, st2, st0);
+      if (s + 2 >= stages) break;
+      turn(s + 2, st2, st3, st1);
+      if (s + 3 >= stages) break;
+      turn(s + 3, st3, st0, st2);
+      if (s + 4 >= stages) break;
+    }
+    wait_and_meet<0>();  // the stages' memory is used again below
+  }
+
+  // A lane has row lane & 31 of y and 4 consecutive columns in each quarter
+  // of a result: 32 rows at a time go through LDS (this wave's own part) and
+  // leave as whole 16-byte pieces.  Results are rounded once, here.
+  constexpr uint32_t kRow = 32 * FN * sizeof(T), kPitch = kRow + 16;
+  static_assert((WN + 1) / 2 * 32 * kPitch <= sizeof(St), "the stage holds the results");
+  uint8_t* out = reinterpret_cast<uint8_t*>((wave & 3) == 0   ? &st0
+                                             : (wave & 3) == 1 ? &st1
+                                             : (wave & 3) == 2 ? &st2
+                                                               : &st3) +
+                 (wave >> 2) * 32 * kPitch;
+  const uint32_t nw = n0 + wn * 32 * FN;
+#pragma unroll
+  for (int i = 0; i < FM; i++) {
+#pragma unroll
+    for (int j = 0; j < FN; j++)
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        T v[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) v[u] = (T)acc[i][j][4 * q + u];
+        __builtin_memcpy(out + r * kPitch + (j * 32 + q * 8 + g * 4) * sizeof(T), v, sizeof(v));
+      }
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    constexpr uint32_t kLanes = kRow / 16, kRows = 64 / kLanes, kE = 16 / sizeof(T);
+#pragma unroll
+    for (uint32_t q = 0; q < 32 / kRows; q++) {
+      const uint32_t row = q * kRows + lane / kLanes, col = (lane % kLanes) * kE;
+      const uint64_t m = m0 + wm * 32 * FM + i * 32 + row;
+      T v[kE];
+      __builtin_memcpy(v, __builtin_assume_aligned(out + row * kPitch + col * sizeof(T), 16), 16);
+      if (m < m_end) {
+        T* to = y + m * p.cols + nw + col;
+        if (nw + col + kE <= p.cols) {
+          __builtin_memcpy(to, v, 16);
+        } else {
+#pragma unroll
+          for (uint32_t u = 0; u < kE; u++)
+            if (nw + col + u < p.cols) to[u] = v[u];
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+
+// Up to 16 rows (of a group) at a time against 16 columns a workgroup: what
+// counts is reading b once, at full bandwidth.  The waves divide the
+// contraction in pieces of 512 elements; a lane loads 16 bytes of a row of b
+// and an instruction's 4 lanes of a row 64 bytes, straight into registers.
+// With x unquantized (T), the workgroup quantizes its rows into LDS first,
+// while the first loads of b are in flight.
+constexpr uint32_t kFewCols = 16, kFewRows = 16, kFewWaves = 8;
+constexpr uint32_t kPiece = 512;
+
+__device__ __forceinline__ f32x4 multiply16(const i32x4& b, const i32x4& a, f32x4 acc, int sb,
+                                            int sa) {
+  const i32x8 wb = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+  const i32x8 wa = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wb, wa, acc, kFp4, kFp4, 0, sb, 0, sa);
+}
+
+struct Few {
+  const void* x;
+  uint64_t stride;
+  uint32_t raw_depth;  // elements of a row of x
+  Operand a;           // x in the 4-bit form, where it is
+  Operand b;
+  void* y;
+  const int32_t* offsets;
+  uint64_t rows;
+  uint32_t cols, depth, experts, n_tiles;
+  uint32_t held;  // rows that LDS holds (quantized here)
+};
+
+template <typename T, bool QUANTIZE>
+__global__ __launch_bounds__(64 * kFewWaves) void mx_few(const Few p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ float part[kFewWaves][256];
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const uint32_t waves = blockDim.x >> 6;
+  const uint32_t r = lane & 15, g = lane >> 4;
+  const uint32_t tn = blockIdx.x % p.n_tiles, e = blockIdx.x / p.n_tiles;
+  const uint32_t n0 = tn * kFewCols;
+  uint64_t first = 0, count = p.rows;
+  T* y = (T*)p.y;
+  const uint8_t *bc = p.b.codes, *bs = p.b.scales;
+  if (p.experts) {
+    if (e == p.experts) {  // rows of no group: zeros
+      int64_t f = p.offsets[p.experts];
+      f = f < 0 ? 0 : f;
+      const uint32_t col = n0 + threadIdx.x % kFewCols;
+      if (col < p.cols)
+        for (uint64_t m = (uint64_t)f + threadIdx.x / kFewCols; m < p.rows;
+             m += blockDim.x / kFewCols)
+          y[m * p.cols + col] = (T)0.0f;
+      return;
+    }
+    group_rows(p.offsets, e, p.rows, first, count);
+    if (count == 0) return;
+    bc += (uint64_t)e * p.cols * (p.depth / 2);
+    bs += (uint64_t)e * p.cols * (p.depth / 32);
+  }
+  const uint32_t pitch = p.depth / 2, spitch = p.depth / 32;
+  const uint32_t steps = p.depth / 128, pieces = (steps + 3) / 4;
+  const uint32_t n = min(n0 + r, p.cols - 1);
+  const uint8_t* gb = bc + (uint64_t)n * pitch + g * 16;
+  const uint8_t* gsb = bs + (uint64_t)n * spitch + g;
+  const uint32_t lpitch = pitch + 16;  // rows of LDS start 4 banks apart
+  uint8_t* lscales = lds + p.held * lpitch;
+
+  for (uint64_t m0 = 0; m0 < count; m0 += QUANTIZE ? p.held : kFewRows) {
+    const uint32_t here = (uint32_t)min((uint64_t)(QUANTIZE ? p.held : kFewRows), count - m0);
+    i32x4 fb[4];
+    int sb[4];
+    uint32_t piece = wave;
+    auto load = [&](uint32_t at) {
+#pragma unroll
+      for (int s = 0; s < 4; s++) {  // steps past the end read the last one
+        const uint32_t step = min(at * 4 + s, steps - 1);
+        fb[s] = *reinterpret_cast<const i32x4*>(gb + step * 64);
+        sb[s] = gsb[step * 4];
+      }
+    };
+    if (piece < pieces) load(piece);
+    const uint64_t row0 = first + m0;
+    const uint32_t lr = min(r, here - 1);
+    const uint8_t *ga, *gsa;
+    if constexpr (QUANTIZE) {
+      const uint32_t chunks = p.depth / 8;
+      __syncthreads();  // the rows before are done
+      for (uint32_t i = threadIdx.x; i < here * chunks; i += blockDim.x) {
+        const uint32_t row = i / chunks, c = i - row * chunks;  // quads of lanes share a block
+        const Eight<T> v = load_eight((const T*)p.x + (row0 + row) * p.stride + c * 8,
+                                      (int64_t)p.raw_depth - c * 8);
+        const uint32_t s = scale_byte(exponent_of<T>(max_of_4_lanes(magnitude_of_eight(v))));
+        *reinterpret_cast<uint32_t*>(lds + row * lpitch + c * 4) = code_eight(v, scale_of(s));
+        if ((c & 3) == 0) lscales[row * spitch + c / 4] = (uint8_t)s;
+      }
+      __syncthreads();
+      ga = lds + lr * lpitch + g * 16;
+      gsa = lscales + lr * spitch + g;
+    } else {
+      ga = p.a.codes + (row0 + lr) * pitch + g * 16;
+      gsa = p.a.scales + (row0 + lr) * spitch + g;
+    }
+    f32x4 acc = {};
+    while (piece < pieces) {
+      i32x4 wb[4];
+      int ws[4];
+#pragma unroll
+      for (int s = 0; s < 4; s++) wb[s] = fb[s], ws[s] = sb[s];
+      const uint32_t now = piece;
+      piece += waves;
+      if (piece < pieces) load(piece);
+#pragma unroll
+      for (int s = 0; s < 4; s++) {
+        const uint32_t step = now * 4 + s;
+        if (step < steps) {
+          const i32x4 fa = *reinterpret_cast<const i32x4*>(ga + step * 64);
+          acc = multiply16(wb[s], fa, acc, ws[s], gsa[step * 4]);
+        }
+      }
+    }
+    // a lane has row r of y and columns 4 g .. 4 g + 3; the waves' parts are
+    // added in their order
+    *reinterpret_cast<f32x4*>(&part[wave][r * 16 + g * 4]) = acc;
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < here * 16; i += blockDim.x) {
+      float sum = 0;
+      for (uint32_t w = 0; w < waves; w++) sum += part[w][i];
+      const uint32_t col = n0 + (i & 15);
+      if (col < p.cols) y[(row0 + (i >> 4)) * p.cols + col] = (T)sum;
+    }
+    if (m0 + (QUANTIZE ? p.held : kFewRows) < count) __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+ec_status launched() { return hipGetLastError() == hipSuccess ? EC_OK : EC_ERR_DEVICE; }
+
+template <int FM, int FN, int WN, typename T, int MODE>
+ec_status tiles_as(Product p, hipStream_t s) {
+  p.n_tiles = (uint32_t)ceil_div(p.cols, 32 * FN * WN);
+  uint64_t m = ceil_div(p.rows, 64 * FM);
+  // groups round up each, and the rows of no group once more
+  if (MODE == kExperts) m += (p.experts < p.rows ? p.experts : p.rows) + 1;
+  const uint64_t tiles = m * p.n_tiles * (MODE == kTokens ? p.experts : 1);
+  if (tiles > 0x7ffffff0ull) return EC_ERR_UNSUPPORTED;
+  p.m_tiles = (uint32_t)m;
+  hipLaunchKernelGGL((mx_tiles<FM, FN, WN, T, MODE>), dim3((uint32_t)ceil_div(tiles, 8) * 8),
+                     dim3(128 * WN), 0, s, p);
+  return launched();
+}
+
+template <typename T, int MODE>
+ec_status tiles_of(const Product& p, hipStream_t s) {
+  const uint64_t groups = MODE == kTokens ? p.experts : 1;
+  // the larger tile reads less, as long as it leaves work for every unit
+  if (ceil_div(p.rows, 256) * ceil_div(p.cols, 256) * groups >= 192)
+    return tiles_as<4, 2, 4, T, MODE>(p, s);
+  if (ceil_div(p.rows, 128) * ceil_div(p.cols, 128) * groups >= 128)
+    return tiles_as<2, 2, 2, T, MODE>(p, s);
+  return tiles_as<1, 1, 2, T, MODE>(p, s);
+}
+
+template <int MODE>
+ec_status tiles(const Product& p, int type, hipStream_t s) {
+  switch (type) {
+    case EC_TYPE_F32: return tiles_of<float, MODE>(p, s);
+    case EC_TYPE_F16: return tiles_of<f16_t, MODE>(p, s);
+    default: return tiles_of<bf16_t, MODE>(p, s);
+  }
+}
+
+template <typename T>
+ec_status few_of(const Few& p, bool quantize, hipStream_t s) {
+  const uint64_t blocks = (uint64_t)p.n_tiles * (p.experts ? p.experts + 1 : 1);
+  if (blocks > 0x7fffffffull) return EC_ERR_UNSUPPORTED;
+  const uint32_t pieces = (p.depth + kPiece - 1) / kPiece;
+  const uint32_t waves = pieces < kFewWaves ? pieces : kFewWaves;
+  const uint32_t lds = quantize ? p.held * (p.depth / 2 + 16 + p.depth / 32) : 0;
+  if (quantize)
+    hipLaunchKernelGGL((mx_few<T, true>), dim3((uint32_t)blocks), dim3(64 * waves), lds, s, p);
+  else
+    hipLaunchKernelGGL((mx_few<T, false>), dim3((uint32_t)blocks), dim3(64 * waves), lds, s, p);
+  return launched();
+}
+
+ec_status few(const Few& p, int type, bool quantize, hipStream_t s) {
+  switch (type) {
+    case EC_TYPE_F32: return few_of<float>(p, quantize, s);
+    case EC_TYPE_F16: return few_of<f16_t>(p, quantize, s);
+    default: return few_of<bf16_t>(p, quantize, s);
+  }
+}
+
+bool form_ok(const void* codes, const void* scales) {
+  return codes && scales && aligned(codes, 16) && aligned(scales, 16);
+}
+
+ec_status check(const void* a, const void* sa, uint64_t rows, const void* b, const void* sb,
+                uint64_t cols, uint64_t depth, const void* y, int type) {
+  if (!type_known(type) || cols == 0 || depth % 128 != 0) return EC_ERR_INVALID;
+  if (rows > EC_MX_MAX_ROWS || cols > EC_MX_MAX_ROWS || depth > EC_MX_MAX_DEPTH)
+    return EC_ERR_UNSUPPORTED;
+  if (rows == 0) return EC_OK;
+  if (!y || !aligned(y, type_bytes(type))) return EC_ERR_INVALID;
+  if (depth && (!form_ok(b, sb) || !form_ok(a, sa))) return EC_ERR_INVALID;
+  return EC_OK;
+}
+
+ec_status check_groups(const int32_t* offsets, uint32_t groups) {
+  if (!offsets || !aligned(offsets, 4) || groups == 0) return EC_ERR_INVALID;
+  return groups > EC_MX_MAX_GROUPS ? EC_ERR_UNSUPPORTED : EC_OK;
+}
+
+// How ec_mx_linear goes: rows (on average of a group) up to kFewRows take the
+// kernel for few rows.
+enum Way { kFewQuantizing, kFewStored, kTiled };
+constexpr uint32_t kFewLds = 48 * 1024;
+
+uint32_t held_rows(uint64_t rows, uint64_t padded) {
+  const uint64_t each = padded / 2 + 16 + padded / 32;
+  uint64_t n = kFewLds / each;
+  if (n > kFewRows) n = kFewRows;
+  return (uint32_t)(n < rows ? n : rows);
+}
+
+Way way_of(uint64_t rows, uint64_t padded, uint32_t experts) {
+  const uint64_t mean = experts ? ceil_div(rows, experts) : rows;
+  if (mean > kFewRows) return kTiled;
+  return mean <= 8 && held_rows(rows, padded) >= mean ? kFewQuantizing : kFewStored;
+}
+
+}  // namespace
+
+extern "C" {
+
+ec_status ec_mx_product(const void* a_codes, const void* a_scales, uint64_t rows,
+                        const void* b_codes, const void* b_scales, uint64_t cols, uint64_t depth,
+                        void* y, int type, void* stream) {
+  const ec_status st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, y, type);
+  if (st != EC_OK || rows == 0) return st;
+  if (depth == 0) return EC_ERR_INVALID;
+  if (rows <= kFewRows) {
+    Few f{};
+    f.a = {(const uint8_t*)a_codes, (const uint8_t*)a_scales};
+    f.b = {(const uint8_t*)b_codes, (const uint8_t*)b_scales};
+    f.y = y, f.rows = rows, f.cols = (uint32_t)cols, f.depth = (uint32_t)depth;
+    f.n_tiles = (uint32_t)ceil_div(cols, kFewCols);
+    return few(f, type, false, (hipStream_t)stream);
+  }
+  Product p{};
+  p.a = {(const uint8_t*)a_codes, (const uint8_t*)a_scales};
+  p.b = {(const uint8_t*)b_codes, (const uint8_t*)b_scales};
+  p.y = y, p.rows = rows, p.cols = (uint32_t)cols, p.depth = (uint32_t)depth;
+  return tiles<kDense>(p, type, (hipStream_t)stream);
+}
+
+ec_status ec_mx_product_experts(const void* a_codes, const void* a_scales, uint64_t rows,
+                                const void* b_codes, const void* b_scales, uint64_t cols,
+                                uint64_t depth, const int32_t* offsets, uint32_t experts, void* y,
+                                int type, void* stream) {
+  ec_status st = check_groups(offsets, experts);
+  if (st != EC_OK) return st;
+  st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, y, type);
+  if (st != EC_OK || rows == 0) return st;
+  if (depth == 0) return EC_ERR_INVALID;
+  if (ceil_div(rows, experts) <= kFewRows) {
+    Few f{};
+    f.a = {(const uint8_t*)a_codes, (const uint8_t*)a_scales};
+    f.b = {(const uint8_t*)b_codes, (const uint8_t*)b_scales};
+    f.y = y, f.rows = rows, f.cols = (uint32_t)cols, f.depth = (uint32_t)depth;
+    f.offsets = offsets, f.experts = experts;
+    f.n_tiles = (uint32_t)ceil_div(cols, kFewCols);
+    return few(f, type, false, (hipStream_t)stream);
+  }
+  Product p{};
+  p.a = {(const uint8_t*)a_codes, (const uint8_t*)a_scales};
+  p.b = {(const uint8_t*)b_codes, (const uint8_t*)b_scales};
+  p.y = y, p.rows = rows, p.cols = (uint32_t)cols, p.depth = (uint32_t)depth;
+  p.offsets = offsets, p.experts = experts;
+  return tiles<kExperts>(p, type, (hipStream_t)stream);
+}
+
+ec_status ec_mx_product_tokens(const void* a_codes, const void* a_scales, uint64_t rows,
+                               const void* b_codes, const void* b_scales, uint64_t cols,
+                               uint64_t tokens, const int32_t* offsets, uint32_t experts, void* y,
+                               int type, void* stream) {
+  ec_status st = check_groups(offsets, experts);
+  if (st != EC_OK) return st;
+  if (tokens > EC_MX_MAX_ROWS) return EC_ERR_UNSUPPORTED;
+  const uint64_t depth = ec_mx_padded_groups(tokens, experts);
+  st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, y, type);
+  if (st != EC_OK || rows == 0) return st;
+  Product p{};
+  p.a = {(const uint8_t*)a_codes, (const uint8_t*)a_scales};
+  p.b = {(const uint8_t*)b_codes, (const uint8_t*)b_scales};
+  p.y = y, p.rows = rows, p.cols = (uint32_t)cols, p.depth = (uint32_t)depth;
+  p.offsets = offsets, p.experts = experts, p.tokens = tokens;
+  return tiles<kTokens>(p, type, (hipStream_t)stream);
+}
+
+size_t ec_mx_linear_workspace_bytes(uint64_t rows, uint64_t depth, uint64_t cols,
+                                    uint32_t experts) {
+  (void)cols;
+  const uint64_t padded = ec_mx_padded(depth);
+  if (rows == 0 || way_of(rows, padded, experts) == kFewQuantizing) return 0;
+  return (rows * (padded / 2) + 15) / 16 * 16 + rows * (padded / 32);
+}
+
+ec_status ec_mx_linear(const void* x, int type, uint64_t rows, uint64_t depth, uint64_t stride,
+                       const void* w_codes, const void* w_scales, uint64_t cols,
+                       const int32_t* offsets, uint32_t experts, void* y, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (!type_known(type) || depth == 0 || cols == 0 || stride < depth || (!offsets) != (!experts))
+    return EC_ERR_INVALID;
+  if (experts > EC_MX_MAX_GROUPS || rows > EC_MX_MAX_ROWS || cols > EC_MX_MAX_ROWS ||
+      depth > EC_MX_MAX_DEPTH)
+    return EC_ERR_UNSUPPORTED;
+  if (rows == 0) return EC_OK;
+  if (!x || !aligned(x, type_bytes(type)) || !y || !aligned(y, type_bytes(type)) ||
+      !form_ok(w_codes, w_scales) || !aligned(offsets, 4) || !aligned(workspace, 16))
+    return EC_ERR_INVALID;
+  const size_t need = ec_mx_linear_workspace_bytes(rows, depth, cols, experts);
+  if (need && !workspace) return EC_ERR_INVALID;
+  if (workspace_bytes < need) return EC_ERR_CAPACITY;
+  const uint64_t padded = ec_mx_padded(depth);
+  const Way way = way_of(rows, padded, experts);
+  if (way == kFewQuantizing) {
+    Few f{};
+    f.x = x, f.stride = stride, f.raw_depth = (uint32_t)depth;
+    f.b = {(const uint8_t*)w_codes, (const uint8_t*)w_scales};
+    f.y = y, f.rows = rows, f.cols = (uint32_t)cols, f.depth = (uint32_t)padded;
+    f.offsets = offsets, f.experts = experts;
+    f.n_tiles = (uint32_t)ceil_div(cols, kFewCols);
+    f.held = held_rows(rows, padded);
+    return few(f, type, true, (hipStream_t)stream);
+  }
+  uint8_t* codes = (uint8_t*)workspace;
+  uint8_t* scales = codes + (rows * (padded / 2) + 15) / 16 * 16;
+  const ec_status st = ec_mx_quantize(x, type, rows, depth, stride, codes, scales, stream);
+  if (st != EC_OK) return st;
+  if (experts)
+    return ec_mx_product_experts(codes, scales, rows, w_codes, w_scales, cols, padded, offsets,
+                                 experts, y, type, stream);
+  return ec_mx_product(codes, scales, rows, w_codes, w_scales, cols, padded, y, type, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,296 @@
+"""The microscaled 4-bit floating-point format on gfx950 (include/ec_mx.h):
+quantization, its inverse, products of 4-bit operands, and the training steps
+of a layer and of an expert layer built from them.
+
+Like the rest of the binding this module only checks and marshals arguments;
+every step runs in the library's kernels on torch's current stream of the
+tensors' device, or on `stream`, on which the results are then allocated (the
+caller orders that stream after what produced the inputs).
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _binding as _b
+from ._binding import EC_ERR_INVALID, ECError
+
+TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _refuse(what: str):
+    raise ECError(EC_ERR_INVALID, what)
+
+
+def _type(t: torch.Tensor, what: str) -> int:
+    code = TYPES.get(t.dtype)
+    if code is None or not t.is_cuda:
+        _refuse(f"{what}: a float32, float16 or bfloat16 tensor on the GPU is wanted")
+    return code
+
+
+def _rows(x: torch.Tensor) -> torch.Tensor:
+    """x as [rows, cols] with unit column stride (a copy only where its strides allow no view)."""
+    if x.dim() != 2:
+        x = x.reshape(-1, x.shape[-1])
+    return x if x.stride(1) == 1 and x.stride(0) >= x.shape[1] else x.contiguous()
+
+
+def padded(cols: int) -> int:
+    return (cols + 127) // 128 * 128
+
+
+class MXTensor:
+    """A tensor in the 4-bit form along its last dimension, of `cols` elements:
+    codes, uint8 [..., padded / 2], and scales, uint8 [..., padded / 32]."""
+
+    __slots__ = ("codes", "scales", "cols")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
+        p = (cols + 127) // 128 * 128
+        if (codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or cols < 0
+                or codes.shape[-1] * 2 != p or scales.shape[-1] * 32 != p
+                or codes.shape[:-1] != scales.shape[:-1]
+                or not codes.is_contiguous() or not scales.is_contiguous()
+                or codes.device != scales.device):
+            _refuse("MXTensor: uint8 codes [..., padded / 2] and scales [..., padded / 32], "
+                    "contiguous and on one device, are wanted")
+        self.codes, self.scales, self.cols = codes, scales, cols
+
+    @property
+    def shape(self) -> torch.Size:
+        return self.codes.shape[:-1] + (self.cols,)
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    def numel_bytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def _made(codes, scales, cols) -> MXTensor:
+    m = object.__new__(MXTensor)
+    m.codes, m.scales, m.cols = codes, scales, cols
+    return m
+
+
+def _empty(lead, cols, device, p=None) -> MXTensor:
+    p = (cols + 127) // 128 * 128 if p is None else p
+    return _made(torch.empty((*lead, p // 2), dtype=torch.uint8, device=device),
+                 torch.empty((*lead, p // 32), dtype=torch.uint8, device=device), cols)
+
+
+def mx_quantize(x: torch.Tensor, stream=None) -> MXTensor:
+    """x [..., cols] in the 4-bit form along its last dimension."""
+    if stream is not None or _b.elsewhere(x):
+        return _b.on_stream(mx_quantize, (x,), stream)
+    kind = _type(x, "mx_quantize")
+    if x.dim() == 0 or x.shape[-1] == 0:
+        _refuse("mx_quantize: at least one element a row is wanted")
+    r = _rows(x)
+    q = _empty(x.shape[:-1], x.shape[-1], x.device)
+    _b.check(_b.lib().ec_mx_quantize(r.data_ptr(), kind, r.shape[0], r.shape[1], r.stride(0),
+                                     q.codes.data_ptr(), q.scales.data_ptr(),
+                                     _b.current_stream(x)), "ec_mx_quantize")
+    return q
+
+
+def mx_quantize_both(x: torch.Tensor, stream=None) -> tuple[MXTensor, MXTensor]:
+    """x [rows, cols] or [batch, rows, cols] along its rows, and transposed along its columns
+    ([..., cols, rows]), in one pass over x."""
+    if stream is not None or _b.elsewhere(x):
+        return _b.on_stream(mx_quantize_both, (x,), stream)
+    kind = _type(x, "mx_quantize_both")
+    if x.dim() not in (2, 3) or x.shape[-1] == 0:
+        _refuse("mx_quantize_both: [rows, cols] or [batch, rows, cols] is wanted")
+    rows, cols = x.shape[-2:]
+    if x.stride(-1) != 1 or x.stride(-2) < cols or (x.dim() == 3 and x.stride(0) < 0):
+        x = x.contiguous()
+    lead = x.shape[:-2]
+    batch = x.shape[0] if x.dim() == 3 else 1
+    a, b = _empty((*lead, rows), cols, x.device), _empty((*lead, cols), rows, x.device)
+    if rows and batch:
+        _b.check(_b.lib().ec_mx_quantize_both(
+            x.data_ptr(), kind, batch, rows, cols, x.stride(0) if x.dim() == 3 else 0, x.stride(-2),
+            a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
+            _b.current_stream(x)), "ec_mx_quantize_both")
+    return a, b
+
+
+def mx_dequantize(q: MXTensor, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+    """The values that q holds, rounded once to dtype."""
+    if stream is not None or _b.elsewhere(q.codes):
+        return _b.on_stream(mx_dequantize, (q, dtype), stream)
+    kind = TYPES.get(dtype)
+    if kind is None or not q.codes.is_cuda or q.cols == 0:
+        _refuse("mx_dequantize: a nonempty row on the GPU and float32, float16 or bfloat16 are wanted")
+    lead = q.codes.shape[:-1]
+    y = torch.empty((*lead, q.cols), dtype=dtype, device=q.codes.device)
+    rows = y.numel() // q.cols
+    _b.check(_b.lib().ec_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), rows, q.cols,
+                                       y.data_ptr(), kind, q.cols, _b.current_stream(y)),
+             "ec_mx_dequantize")
+    return y
+
+
+def _offsets(offsets: torch.Tensor, groups: int, device, what: str) -> torch.Tensor:
+    if (offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous()
+            or offsets.shape[0] != groups + 1 or offsets.device != device):
+        _refuse(f"{what}: int32 offsets [experts + 1] on the tensors' device are wanted")
+    return offsets
+
+
+def mx_product(a: MXTensor, b: MXTensor, dtype: torch.dtype = torch.bfloat16,
+               stream=None) -> torch.Tensor:
+    """a b^T [rows, cols] of a [rows, depth] and b [cols, depth], summed in fp32, rounded once."""
+    if stream is not None or _b.elsewhere(a.codes):
+        return _b.on_stream(mx_product, (a, b, dtype), stream)
+    kind = TYPES.get(dtype)
+    if (kind is None or a.codes.dim() != 2 or b.codes.dim() != 2 or a.cols != b.cols or a.cols == 0
+            or not a.codes.is_cuda or a.codes.device != b.codes.device):
+        _refuse("mx_product: [rows, depth] and [cols, depth] on one GPU are wanted")
+    rows, cols = a.codes.shape[0], b.codes.shape[0]
+    y = torch.empty((rows, cols), dtype=dtype, device=a.codes.device)
+    _b.check(_b.lib().ec_mx_product(a.codes.data_ptr(), a.scales.data_ptr(), rows,
+                                    b.codes.data_ptr(), b.scales.data_ptr(), cols,
+                                    a.codes.shape[1] * 2, y.data_ptr(), kind,
+                                    _b.current_stream(y)), "ec_mx_product")
+    return y
+
+
+def _linear(x, w, offsets, experts, what):
+    kind = _type(x, what)
+    cols, depth = w.codes.shape[-2], x.shape[-1]
+    if w.cols != depth or depth == 0 or w.codes.device != x.device:
+        _refuse(f"{what}: weights [.., cols, depth] on the device of x [.., depth] are wanted")
+    r = _rows(x)
+    rows = r.shape[0]
+    L = _b.lib()
+    y = torch.empty((*x.shape[:-1], cols), dtype=x.dtype, device=x.device)
+    need = L.ec_mx_linear_workspace_bytes(rows, depth, cols, experts)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device).data_ptr() if need else None
+    _b.check(L.ec_mx_linear(r.data_ptr(), kind, rows, depth, r.stride(0), w.codes.data_ptr(),
+                            w.scales.data_ptr(), cols,
+                            offsets.data_ptr() if experts else None, experts, y.data_ptr(), ws,
+                            need, _b.current_stream(x)), "ec_mx_linear")
+    return y
+
+
+def mx_linear(x: torch.Tensor, w: MXTensor, stream=None) -> torch.Tensor:
+    """x w^T with x [..., depth] quantized on the way and weights w [cols, depth]."""
+    if stream is not None or _b.elsewhere(x):
+        return _b.on_stream(mx_linear, (x, w), stream)
+    if w.codes.dim() != 2:
+        _refuse("mx_linear: weights [cols, depth] are wanted")
+    return _linear(x, w, None, 0, "mx_linear")
+
+
+def mx_experts_linear(x: torch.Tensor, w: MXTensor, offsets: torch.Tensor,
+                      stream=None) -> torch.Tensor:
+    """Rows x [rows, depth] sorted by expert, rows [offsets[e], offsets[e + 1]) times the weights
+    of expert e, w [experts, cols, depth]; zeros in rows of no expert."""
+    if stream is not None or _b.elsewhere(x):
+        return _b.on_stream(mx_experts_linear, (x, w, offsets), stream)
+    if w.codes.dim() != 3 or x.dim() != 2:
+        _refuse("mx_experts_linear: x [rows, depth] and weights [experts, cols, depth] are wanted")
+    experts = w.codes.shape[0]
+    _offsets(offsets, experts, x.device, "mx_experts_linear")
+    return _linear(x, w, offsets, experts, "mx_experts_linear")
+
+
+class MXLinearSaved:
+    """What the backward pass of a 4-bit layer needs: its input and weights along their columns
+    (17/32 of a byte an element), and for experts the offsets."""
+
+    __slots__ = ("x", "w", "offsets", "rows", "dtype")
+
+    def __init__(self, x, w, offsets, rows, dtype):
+        self.x, self.w, self.offsets, self.rows, self.dtype = x, w, offsets, rows, dtype
+
+
+def mx_linear_forward(x: torch.Tensor, w: torch.Tensor, stream=None):
+    """y = Q(x) Q(w)^T of x [rows, depth] and w [cols, depth], and what the backward needs."""
+    if stream is not None or _b.elsewhere(x):
+        return _b.on_stream(mx_linear_forward, (x, w), stream)
+    if (x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or x.dtype != w.dtype
+            or x.device != w.device or w.shape[0] == 0):
+        _refuse("mx_linear_forward: x [rows, depth] and w [cols, depth] of one type are wanted")
+    xr, xc = mx_quantize_both(x)
+    wr, wc = mx_quantize_both(w)
+    return mx_product(xr, wr, x.dtype), MXLinearSaved(xc, wc, None, x.shape[0], x.dtype)
+
+
+def mx_linear_backward(dy: torch.Tensor, saved: MXLinearSaved, stream=None):
+    """dx = Q(dy) Q(w^T)^T and dw = Q(dy^T) Q(x^T)^T, blocks along the summed dimension."""
+    if stream is not None or _b.elsewhere(dy):
+        return _b.on_stream(mx_linear_backward, (dy, saved), stream)
+    if (saved.offsets is not None or dy.dim() != 2 or dy.dtype != saved.dtype
+            or dy.shape != (saved.rows, saved.w.cols) or dy.device != saved.x.device):
+        _refuse("mx_linear_backward: dy [rows, cols] of the forward's type is wanted")
+    if saved.rows == 0:
+        return (dy.new_zeros(0, saved.x.codes.shape[0]),
+                dy.new_zeros(dy.shape[1], saved.x.codes.shape[0]))
+    dr, dc = mx_quantize_both(dy)
+    return mx_product(dr, saved.w, dy.dtype), mx_product(dc, saved.x, dy.dtype)
+
+
+def _quantize_groups(x, offsets, experts, rows_too=True):
+    r = x if x.stride(1) == 1 and x.stride(0) >= x.shape[1] else x.contiguous()
+    rows, cols = x.shape
+    L = _b.lib()
+    a = _empty((rows,), cols, x.device)
+    b = _empty((cols,), rows, x.device, int(L.ec_mx_padded_groups(rows, experts)))
+    if rows:
+        _b.check(L.ec_mx_quantize_groups(r.data_ptr(), TYPES[x.dtype], rows, cols, r.stride(0),
+                                         offsets.data_ptr(), experts, a.codes.data_ptr(),
+                                         a.scales.data_ptr(), b.codes.data_ptr(),
+                                         b.scales.data_ptr(), _b.current_stream(x)),
+                 "ec_mx_quantize_groups")
+    return a, b
+
+
+def _experts_product(a, b, offsets, dtype):
+    experts, cols = b.codes.shape[:2]
+    rows = a.codes.shape[0]
+    y = torch.empty((rows, cols), dtype=dtype, device=a.codes.device)
+    _b.check(_b.lib().ec_mx_product_experts(
+        a.codes.data_ptr(), a.scales.data_ptr(), rows, b.codes.data_ptr(), b.scales.data_ptr(), cols,
+        a.codes.shape[1] * 2, offsets.data_ptr(), experts, y.data_ptr(), TYPES[dtype],
+        _b.current_stream(y)), "ec_mx_product_experts")
+    return y
+
+
+def mx_experts_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, stream=None):
+    """The training forward of mx_experts_linear from weights w [experts, cols, depth] of x's type;
+    the blocks of the saved columns begin anew at every expert's first row."""
+    if stream is not None or _b.elsewhere(x):
+        return _b.on_stream(mx_experts_forward, (x, w, offsets), stream)
+    _type(x, "mx_experts_forward")
+    if (x.dim() != 2 or w.dim() != 3 or x.shape[1] != w.shape[2] or x.dtype != w.dtype
+            or x.device != w.device or 0 in w.shape):
+        _refuse("mx_experts_forward: x [rows, depth] and w [experts, cols, depth] of one type are wanted")
+    _offsets(offsets, w.shape[0], x.device, "mx_experts_forward")
+    xr, xc = _quantize_groups(x, offsets, w.shape[0])
+    wr, wc = mx_quantize_both(w)
+    return (_experts_product(xr, wr, offsets, x.dtype),
+            MXLinearSaved(xc, wc, offsets, x.shape[0], x.dtype))
+
+
+def mx_experts_backward(dy: torch.Tensor, saved: MXLinearSaved, stream=None):
+    """dx [rows, depth] and dw [experts, cols, depth]; rows of no expert give zeros and take no
+    part, an expert without rows gets zeros."""
+    if stream is not None or _b.elsewhere(dy):
+        return _b.on_stream(mx_experts_backward, (dy, saved), stream)
+    if (saved.offsets is None or dy.dim() != 2 or dy.dtype != saved.dtype
+            or dy.shape != (saved.rows, saved.w.cols) or dy.device != saved.x.device):
+        _refuse("mx_experts_backward: dy [rows, cols] of the forward's type is wanted")
+    experts, depth = saved.w.codes.shape[:2]
+    cols = saved.w.cols
+    dr, dc = _quantize_groups(dy, saved.offsets, experts)
+    dx = _experts_product(dr, saved.w, saved.offsets, dy.dtype)
+    dw = torch.empty((experts, cols, depth), dtype=dy.dtype, device=dy.device)
+    _b.check(_b.lib().ec_mx_product_tokens(
+        dc.codes.data_ptr(), dc.scales.data_ptr(), cols, saved.x.codes.data_ptr(),
+        saved.x.scales.data_ptr(), depth, saved.rows, saved.offsets.data_ptr(), experts,
+        dw.data_ptr(), TYPES[dy.dtype], _b.current_stream(dy)), "ec_mx_product_tokens")
+    return dx, dw
