@@ -244,6 +244,24 @@ __device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, uint32_t 
   return {groups, tile - before, 0, 0};
 }
 
+// Tiles of 2^shift rows that the groups have, and the rows of no group after them.
+__device__ __forceinline__ uint32_t used_tiles(const int32_t* offsets, uint32_t groups,
+                                               uint64_t rows, uint32_t shift) {
+  const uint32_t lane = threadIdx.x & 63;
+  uint64_t sum = 0;
+  for (uint32_t g = lane; g < groups; g += 64) {
+    uint64_t first, count;
+    group_rows(offsets, g, rows, first, count);
+    sum += (count + (1u << shift) - 1) >> shift;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  const int64_t end = offsets[groups];
+  const uint64_t none = end < 0 ? rows : (uint64_t)end < rows ? rows - (uint64_t)end : 0;
+  sum += (none + (1u << shift) - 1) >> shift;
+  return (uint32_t)__builtin_amdgcn_readfirstlane(sum > 0x7fffffffull ? 0x7fffffff : (int)sum);
+}
+
 // Where group e's part of a transposed, padded row starts (in units of 128).
 __device__ __forceinline__ uint32_t group_start(const int32_t* offsets, uint32_t e,
                                                 uint64_t rows) {

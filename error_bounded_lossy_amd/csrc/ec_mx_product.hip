@@ -1,6 +1,8 @@
 // Products of operands in the microscaled 4-bit format (include/ec_mx.h) on
 // the matrix cores' scaled instructions: y = a b^T with both operands stored
 // along the contraction, blocks of 32 sharing a scale.
+#include <type_traits>
+
 #include "ec_mx_device.h"
 
 using namespace ecmx;
@@ -35,15 +37,17 @@ struct Product {
 
 // ---------------------------------------------------------------- tiles
 
-// One workgroup of 2 by WN waves computes a tile of 64 FM rows by 32 FN WN
-// columns, a wave 32 FM by 32 FN of it with 32x32x64 instructions, whose rate
-// measured 8.6 PFLOP/s against 6.8 of the 16x16x128 ones.
+// One workgroup of 2 by 2 waves computes a tile of 64 FM rows by 64 FN columns,
+// a wave 32 FM by 32 FN of it with 32x32x64 instructions, whose rate measured
+// 8.6 PFLOP/s against 6.8 of the 16x16x128 ones.  With FM = FN = 4 a wave's
+// results fill half of its 512 registers, and an operand byte read from LDS is
+// used 128 times.
 //
-// A stage is 128 elements (64 bytes) of every row of both operands plus their
-// 4 scale bytes, brought to LDS without passing registers.  Four stages are in
-// LDS: one is multiplied while the loads of the next three fly, with one
-// barrier a stage, placed before the last multiplications so that they cover
-// the first reads of the next stage.
+// A stage is 128 elements (64 bytes) of every row of both operands, brought to
+// LDS without passing registers.  Four stages are in LDS: one is multiplied
+// while the loads of the next three fly, with one barrier a stage, placed
+// before the last multiplications so that they cover the first reads of the
+// next stage.
 //
 // The order within the contraction is free as long as both operands agree, so
 // lane group g of instruction step s takes the 16-byte chunk 2 g + s of a
@@ -51,20 +55,24 @@ struct Product {
 // step selects its byte in the instruction.  Chunks are stored at their number
 // xor bits 1 and 2 of the row, so that 8 lanes of consecutive rows read 8
 // different 16-byte columns of 128.
+//
+// Scales come 16 bytes a row, once in four stages, through registers: 4 bytes
+// a row and stage would be as many requests of the caches as the codes are
+// (half of the L2 cache's requests, measured).
 template <int BM, int BN>
 struct Stage {
   uint8_t a[BM * 64];
   uint8_t b[BN * 64];
-  uint8_t s[(BM + BN) * 4];  // scales of a, then of b
 };
 
-__device__ __forceinline__ void to_lds16(const uint8_t* from, uint8_t* to) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
-                                   (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+// 16 bytes a lane from base + lane_off + off straight to LDS, 1 KiB from `to` on.
+__device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t base, uint32_t lane_off,
+                                         uint32_t off, uint8_t* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (__attribute__((address_space(3))) void*)to, 16,
+                                           lane_off, off, 0, 0);
 }
-__device__ __forceinline__ void to_lds4(const uint8_t* from, uint8_t* to) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
-                                   (__attribute__((address_space(3))) void*)to, 4, 0, 0);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const uint8_t* p) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0xffffffffu, 0x00027000);
 }
 
 __device__ __forceinline__ i32x8 widened(const i32x4& v) {
@@ -96,25 +104,34 @@ __device__ __forceinline__ void read(const Stage<BM, BN>& st, const Lane& at, in
   for (int i = 0; i < FM; i++)
     f.a[i] = *reinterpret_cast<const i32x4*>(st.a + (at.a ^ (step << 4)) + i * 2048);
 }
-template <int BM, int BN, int FM, int FN>
-__device__ __forceinline__ void read(const Stage<BM, BN>& st, const Lane& at, Scales<FM, FN>& f) {
+// of stage q of the four
+template <int FM, int FN>
+__device__ __forceinline__ void read(const uint8_t* scales, const Lane& at, int q,
+                                     Scales<FM, FN>& f) {
 #pragma unroll
   for (int i = 0; i < FM; i++)
-    f.a[i] = *reinterpret_cast<const uint16_t*>(st.s + at.sa + i * 128);
+    f.a[i] = *reinterpret_cast<const uint16_t*>(scales + at.sa + i * 512 + q * 4);
 #pragma unroll
   for (int i = 0; i < FN; i++)
-    f.b[i] = *reinterpret_cast<const uint16_t*>(st.s + at.sb + i * 128);
+    f.b[i] = *reinterpret_cast<const uint16_t*>(scales + at.sb + i * 512 + q * 4);
 }
 
-template <int FM, int FN, int STEP>
+// `between(i)` issues what goes between the rows of multiplications; nothing
+// else is moved there.
+template <int FM, int FN, int STEP, typename F>
 __device__ __forceinline__ void multiply(const Fragments<FM, FN>& f, const Scales<FM, FN>& s,
-                                         f32x16 (&acc)[FM][FN]) {
+                                         f32x16 (&acc)[FM][FN], F&& between) {
 #pragma unroll
-  for (int i = 0; i < FM; i++)
+  for (int i = 0; i < FM; i++) {
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < FN; j++)
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
           widened(f.b[j]), widened(f.a[i]), acc[i][j], kFp4, kFp4, STEP, s.b[j], STEP, s.a[i]);
+    __builtin_amdgcn_sched_barrier(0);
+    between(i);
+  }
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // Waits until at most N of this wave's loads are under way and its LDS reads
@@ -137,26 +154,30 @@ __device__ __forceinline__ bool tile_of(uint32_t tiles, uint32_t& t) {
   return (blockIdx.x >> 3) < run && t < tiles;
 }
 
-template <int FM, int FN, int WN, typename T, int MODE>
-__global__ __launch_bounds__(128 * WN, 2) void mx_tiles(const Product p) {
-  constexpr int BM = 64 * FM, BN = 32 * FN * WN, kWaves = 2 * WN;
+template <int FM, int FN, typename T, int MODE>
+__global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx_tiles(const Product p) {
+  constexpr int BM = 64 * FM, BN = 64 * FN, kWaves = 4;
   using St = Stage<BM, BN>;
   constexpr uint32_t kShift = FM == 1 ? 6 : FM == 2 ? 7 : 8;
   static_assert((1u << kShift) == BM, "tile rows");
   // four variables, not an array: the compiler then knows which loads a read waits for
   __shared__ __attribute__((aligned(16))) St st0, st1, st2, st3;
+  __shared__ __attribute__((aligned(16))) uint8_t scales[2][(BM + BN) * 16];  // of a, then of b
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t wm = wave & 1, wn = wave >> 1;
 
+  // the tiles that groups have, not the most they could have: each XCD gets its share
+  uint32_t m_tiles = p.m_tiles;
+  if (MODE == kExperts) m_tiles = min(m_tiles, used_tiles(p.offsets, p.experts, p.rows, kShift));
   uint32_t t;
-  if (!tile_of(p.m_tiles * p.n_tiles * (MODE == kTokens ? p.experts : 1), t)) return;
+  if (!tile_of(m_tiles * p.n_tiles * (MODE == kTokens ? p.experts : 1), t)) return;
   uint32_t e = 0;
   if (MODE == kTokens) {
-    e = t / (p.m_tiles * p.n_tiles);
-    t -= e * (p.m_tiles * p.n_tiles);
+    e = t / (m_tiles * p.n_tiles);
+    t -= e * (m_tiles * p.n_tiles);
   }
   const uint32_t width = 8 * p.n_tiles, band = t / width;
-  const uint32_t high = min(p.m_tiles - band * 8, 8u);
+  const uint32_t high = min(m_tiles - band * 8, 8u);
   uint32_t tm = band * 8 + (t - band * width) % high;
   const uint32_t tn = (t - band * width) / high;
 
@@ -181,6 +202,7 @@ __global__ __launch_bounds__(128 * WN, 2) void mx_tiles(const Product p) {
     }
     m0 = gt.first + (uint64_t)gt.local * BM;
     m_end = gt.first + gt.count;
+    if (m0 >= m_end) return;  // only with offsets out of order
     bc += (uint64_t)gt.group * p.cols * (p.depth / 2);
     bs += (uint64_t)gt.group * p.cols * (p.depth / 32);
   }
@@ -214,41 +236,64 @@ __global__ __launch_bounds__(128 * WN, 2) void mx_tiles(const Product p) {
 #pragma unroll
   for (int i = 0; i < LB; i++)
     ob[i] = min((wave * LB + i) * 16 + (lane >> 2), n_last) * pitch + chunk * 16;
-  // scales: 64 rows an instruction; every wave loads the same number of times,
-  // some of them what another one loads too, so that all count alike
-  constexpr int SA = BM / 64, SN = (BM + BN) / 64;  // of a, of both
-  constexpr int kScaleLoads = (SN + kWaves - 1) / kWaves, kLoads = LA + LB + kScaleLoads;
-  const uint8_t* gs[kScaleLoads];
-  uint32_t os[kScaleLoads], ls[kScaleLoads];
-#pragma unroll
-  for (int i = 0; i < kScaleLoads; i++) {
-    const uint32_t q = (wave + kWaves * i) % SN;
-    const bool is_a = q < SA;
-    gs[i] = is_a ? gsa : gsb;
-    os[i] = min((is_a ? q : q - SA) * 64 + lane, is_a ? m_last : n_last) * spitch;
-    ls[i] = q * 256;
-  }
+  constexpr int kLoads = LA + LB;
   const uint32_t stages = __builtin_amdgcn_readfirstlane(k_len / 128);
+  // Scales of stages 4 u .. 4 u + 3: a thread has a row (two rows).  The last
+  // stages may be fewer than four: theirs are loaded first, into `tail`, and
+  // the loop below stays without branches (with them, the compiler moved the
+  // results between registers every turn).  Where there are no four stages at
+  // all, it loads codes that nothing uses.
+  constexpr int kRows = (BM + BN + 255) / 256;
+  const uint32_t fours = stages / 4;
+  const uint8_t* scale_row[kRows];
+  uint4 held[kRows], tail[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; i++) {
+    const uint32_t row = min(threadIdx.x + i * 256, (uint32_t)(BM + BN - 1));
+    scale_row[i] = row < BM ? gsa + min(row, m_last) * spitch
+                            : gsb + min(row - BM, n_last) * spitch;
+    const uint32_t n = stages & 3;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(scale_row[i]) + fours * 4;
+    tail[i] = make_uint4(n > 0 ? w[0] : 0, n > 1 ? w[1] : 0, n > 2 ? w[2] : 0, 0);
+    if (fours == 0) scale_row[i] = p.a.codes;
+  }
+  auto load_scales = [&](uint32_t u) {
+    const uint32_t at = fours ? min(u, fours - 1) * 16 : 0;
+#pragma unroll
+    for (int i = 0; i < kRows; i++) __builtin_memcpy(&held[i], scale_row[i] + at, 16);
+  };
+  auto keep_scales = [&](uint32_t u) {
+#pragma unroll
+    for (int i = 0; i < kRows; i++) {
+      const uint32_t row = threadIdx.x + i * 256;
+      const uint4 v = u < fours ? held[i] : tail[i];
+      if (kRows * 256 == BM + BN || row < BM + BN)
+        *reinterpret_cast<uint4*>(&scales[u & 1][row * 16]) = v;
+    }
+  };
   // Past the last stage it is loaded again, so that every turn below does the
-  // same and waits for the same number of loads.
-  auto load = [&](St& st, uint32_t stage) {
-    uint32_t c = __builtin_amdgcn_readfirstlane(min(stage, stages - 1));
-    // kept a scalar: the compiler would otherwise carry an address per load and lane
-    asm volatile("" : "+s"(c));
+  // same and waits for the same number of loads.  Part i of FM.
+  const __amdgpu_buffer_rsrc_t ra = buffer_at(ga), rb = buffer_at(gb);
+  auto load = [&](St& st, uint32_t stage, int part) {
+    const uint32_t c = __builtin_amdgcn_readfirstlane(min(stage, stages - 1)) * 64;
 #pragma unroll
-    for (int i = 0; i < LA; i++) to_lds16(ga + c * 64 + oa[i], st.a + (wave * LA + i) * 1024);
+    for (int i = part * LA / FM; i < (part + 1) * LA / FM; i++)
+      to_lds16(ra, oa[i], c, st.a + (wave * LA + i) * 1024);
 #pragma unroll
-    for (int i = 0; i < LB; i++) to_lds16(gb + c * 64 + ob[i], st.b + (wave * LB + i) * 1024);
+    for (int i = part * LB / FM; i < (part + 1) * LB / FM; i++)
+      to_lds16(rb, ob[i], c, st.b + (wave * LB + i) * 1024);
+  };
+  auto load_all = [&](St& st, uint32_t stage) {
 #pragma unroll
-    for (int i = 0; i < kScaleLoads; i++) to_lds4(gs[i] + c * 4 + os[i], st.s + ls[i]);
+    for (int i = 0; i < FM; i++) load(st, stage, i);
   };
 
   const uint32_t r = lane & 31, g = lane >> 5;
   Lane at;
   at.a = (wm * 32 * FM + r) * 64 + ((2 * g) ^ ((r >> 1) & 3)) * 16;
   at.b = (wn * 32 * FN + r) * 64 + ((2 * g) ^ ((r >> 1) & 3)) * 16;
-  at.sa = (wm * 32 * FM + r) * 4 + g * 2;
-  at.sb = (BM + wn * 32 * FN + r) * 4 + g * 2;
+  at.sa = (wm * 32 * FM + r) * 16 + g * 2;
+  at.sb = (BM + wn * 32 * FN + r) * 16 + g * 2;
 
   f32x16 acc[FM][FN];
 #pragma unroll
@@ -257,37 +302,52 @@ __global__ __launch_bounds__(128 * WN, 2) void mx_tiles(const Product p) {
     for (int j = 0; j < FN; j++) acc[i][j] = f32x16{};
 
   if (stages > 0) {
-    load(st0, 0);
-    load(st1, 1);
-    load(st2, 2);
+    load_scales(0);
+    load_all(st0, 0);
+    load_all(st1, 1);
+    load_all(st2, 2);
+    keep_scales(0);
     wait_and_meet<2 * kLoads>();
     Fragments<FM, FN> f0, f1;
     Scales<FM, FN> sc;
-    read(st0, at, sc);
+    read(scales[0], at, 0, sc);
     read(st0, at, 0, f0);
-    // Stage s is in `now`; its first fragments and scales are in registers.
-    auto turn = [&](uint32_t s, const St& now, const St& next,
-                    St& free) {
-      load(free, s + 3);
+    // Stage s = 4 u + q is in `now`; its first fragments and scales are in
+    // registers.  The scales of the next four are loaded at q = 0 and in LDS
+    // before the barrier of q = 3; the waits count them as if they were stage
+    // loads, which waits for two more at most.  The last stages (`more`
+    // false) load nothing.
+    auto turn = [&](uint32_t u, auto q, auto more, const St& now, const St& next, St& free) {
+      if (more && q == 3) keep_scales(u + 1);
       read(now, at, 1, f1);
-      multiply<FM, FN, 0>(f0, sc, acc);
-      wait_and_meet<2 * kLoads>();
+      if (more && q == 0) load_scales(u + 1);
+      multiply<FM, FN, 0>(f0, sc, acc, [&](int i) {
+        if (more) load(free, 4 * u + q + 3, i);
+      });
+      if (more) wait_and_meet<2 * kLoads>();
+      else wait_and_meet<0>();
       Scales<FM, FN> snext;
-      read(next, at, snext);
+      read(scales[(q == 3 ? u + 1 : u) & 1], at, (q + 1) & 3, snext);
       read(next, at, 0, f0);
-      multiply<FM, FN, 1>(f1, sc, acc);
+      multiply<FM, FN, 1>(f1, sc, acc, [](int) {});
       sc = snext;
     };
-    for (uint32_t s = 0;; s += 4) {
-      turn(s, st0, st1, st3);
-      if (s + 1 >= stages) break;
-      turn(s + 1, st1, st2, st0);
-      if (s + 2 >= stages) break;
-      turn(s + 2, st2, st3, st1);
-      if (s + 3 >= stages) break;
-      turn(s + 3, st3, st0, st2);
-      if (s + 4 >= stages) break;
+    using std::integral_constant;
+    constexpr integral_constant<int, 0> q0;
+    constexpr integral_constant<int, 1> q1;
+    constexpr integral_constant<int, 2> q2;
+    constexpr integral_constant<int, 3> q3;
+    constexpr std::true_type more;
+    constexpr std::false_type last;
+    for (uint32_t u = 0; u < fours; u++) {
+      turn(u, q0, more, st0, st1, st3);
+      turn(u, q1, more, st1, st2, st0);
+      turn(u, q2, more, st2, st3, st1);
+      turn(u, q3, more, st3, st0, st2);
     }
+    if (stages & 3) turn(fours, q0, last, st0, st1, st3);
+    if ((stages & 3) > 1) turn(fours, q1, last, st1, st2, st0);
+    if ((stages & 3) > 2) turn(fours, q2, last, st2, st3, st1);
     wait_and_meet<0>();  // the stages' memory is used again below
   }
 
@@ -295,12 +355,11 @@ __global__ __launch_bounds__(128 * WN, 2) void mx_tiles(const Product p) {
   // of a result: 32 rows at a time go through LDS (this wave's own part) and
   // leave as whole 16-byte pieces.  Results are rounded once, here.
   constexpr uint32_t kRow = 32 * FN * sizeof(T), kPitch = kRow + 16;
-  static_assert((WN + 1) / 2 * 32 * kPitch <= sizeof(St), "the stage holds the results");
-  uint8_t* out = reinterpret_cast<uint8_t*>((wave & 3) == 0   ? &st0
-                                             : (wave & 3) == 1 ? &st1
-                                             : (wave & 3) == 2 ? &st2
-                                                               : &st3) +
-                 (wave >> 2) * 32 * kPitch;
+  static_assert(32 * kPitch <= sizeof(St), "the stage holds the results");
+  uint8_t* out = reinterpret_cast<uint8_t*>(wave == 0   ? &st0
+                                             : wave == 1 ? &st1
+                                             : wave == 2 ? &st2
+                                                         : &st3);
   const uint32_t nw = n0 + wn * 32 * FN;
 #pragma unroll
   for (int i = 0; i < FM; i++) {
@@ -315,10 +374,10 @@ __global__ __launch_bounds__(128 * WN, 2) void mx_tiles(const Product p) {
       }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    constexpr uint32_t kLanes = kRow / 16, kRows = 64 / kLanes, kE = 16 / sizeof(T);
+    constexpr uint32_t kLanes = kRow / 16, kTogether = 64 / kLanes, kE = 16 / sizeof(T);
 #pragma unroll
-    for (uint32_t q = 0; q < 32 / kRows; q++) {
-      const uint32_t row = q * kRows + lane / kLanes, col = (lane % kLanes) * kE;
+    for (uint32_t q = 0; q < 32 / kTogether; q++) {
+      const uint32_t row = q * kTogether + lane / kLanes, col = (lane % kLanes) * kE;
       const uint64_t m = m0 + wm * 32 * FM + i * 32 + row;
       T v[kE];
       __builtin_memcpy(v, __builtin_assume_aligned(out + row * kPitch + col * sizeof(T), 16), 16);
@@ -476,17 +535,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_few(const Few p) {
 
 ec_status launched() { return hipGetLastError() == hipSuccess ? EC_OK : EC_ERR_DEVICE; }
 
-template <int FM, int FN, int WN, typename T, int MODE>
+template <int FM, int FN, typename T, int MODE>
 ec_status tiles_as(Product p, hipStream_t s) {
-  p.n_tiles = (uint32_t)ceil_div(p.cols, 32 * FN * WN);
+  p.n_tiles = (uint32_t)ceil_div(p.cols, 64 * FN);
   uint64_t m = ceil_div(p.rows, 64 * FM);
   // groups round up each, and the rows of no group once more
   if (MODE == kExperts) m += (p.experts < p.rows ? p.experts : p.rows) + 1;
   const uint64_t tiles = m * p.n_tiles * (MODE == kTokens ? p.experts : 1);
   if (tiles > 0x7ffffff0ull) return EC_ERR_UNSUPPORTED;
   p.m_tiles = (uint32_t)m;
-  hipLaunchKernelGGL((mx_tiles<FM, FN, WN, T, MODE>), dim3((uint32_t)ceil_div(tiles, 8) * 8),
-                     dim3(128 * WN), 0, s, p);
+  hipLaunchKernelGGL((mx_tiles<FM, FN, T, MODE>), dim3((uint32_t)ceil_div(tiles, 8) * 8),
+                     dim3(256), 0, s, p);
   return launched();
 }
 
@@ -495,10 +554,10 @@ ec_status tiles_of(const Product& p, hipStream_t s) {
   const uint64_t groups = MODE == kTokens ? p.experts : 1;
   // the larger tile reads less, as long as it leaves work for every unit
   if (ceil_div(p.rows, 256) * ceil_div(p.cols, 256) * groups >= 192)
-    return tiles_as<4, 2, 4, T, MODE>(p, s);
+    return tiles_as<4, 4, T, MODE>(p, s);
   if (ceil_div(p.rows, 128) * ceil_div(p.cols, 128) * groups >= 128)
-    return tiles_as<2, 2, 2, T, MODE>(p, s);
-  return tiles_as<1, 1, 2, T, MODE>(p, s);
+    return tiles_as<2, 2, T, MODE>(p, s);
+  return tiles_as<1, 1, T, MODE>(p, s);
 }
 
 template <int MODE>
