@@ -153,6 +153,7 @@ struct Shape {
   uint64_t tokens;
   uint32_t cols, chunks, shift, choices;
   uint64_t rows;  // tokens * choices
+  bool past;      // stores go past the caches
 };
 
 struct At {
@@ -183,7 +184,7 @@ template <typename T>
 __device__ __forceinline__ void clear_rows(T* xs, const Shape& s, const At& a, uint64_t none) {
   for (uint64_t r = none + a.token; r < s.rows; r += s.tokens)
     for (uint32_t c = a.lane; c < s.chunks; c += a.lanes)
-      store_eight(xs + r * s.cols + c * 8, (int64_t)s.cols - c * 8, Eight<T>{});
+      store_eight(xs + r * s.cols + c * 8, (int64_t)s.cols - c * 8, Eight<T>{}, s.past);
 }
 
 template <typename T>
@@ -198,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch(const T* __restrict_
     const Eight<T> v = load_eight(x + a.token * s.cols + c * 8, n);
     for (uint32_t j = 0; j < s.choices; j++) {
       const int64_t r = row_of(place, s, a.token, j);
-      if (r >= 0) store_eight(xs + r * s.cols + c * 8, n, v);
+      if (r >= 0) store_eight(xs + r * s.cols + c * 8, n, v, s.past);
     }
   }
   clear_rows(xs, s, a, no_rows(offsets, experts, s.rows));
@@ -264,7 +265,7 @@ __global__ __launch_bounds__(kThreads) void expert_gather(const T* __restrict__ 
         for (int i = 0; i < 8; i++) sum[i] += WEIGHTED ? w[j] * f[i] : f[i];
       }
     }
-    store_eight(y + a.token * s.cols + c * 8, n, narrow<T>(sum));
+    store_eight(y + a.token * s.cols + c * 8, n, narrow<T>(sum), s.past);
   }
 }
 
@@ -320,7 +321,7 @@ __global__ __launch_bounds__(kThreads) void expert_combine_back(
           dot += p;
           if (here && c < s.chunks)
             store_eight(dys + r * s.cols + (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8,
-                        narrow<T>(g));
+                        narrow<T>(g), s.past);
         }
       }
     // the token's lanes together: within a wave by exchange, else over LDS
@@ -345,10 +346,10 @@ ec_status launched() { return hipGetLastError() == hipSuccess ? EC_OK : EC_ERR_D
 
 // `pieces`: how many a lane should have before the row takes more lanes
 Shape shape_of(uint64_t tokens, uint64_t cols, uint32_t choices, uint32_t chunks,
-               uint32_t pieces) {
+               uint32_t pieces, uint64_t bytes_out) {
   Shape s{};
   s.tokens = tokens, s.cols = (uint32_t)cols, s.choices = choices, s.rows = tokens * choices;
-  s.chunks = chunks;
+  s.chunks = chunks, s.past = past_caches(bytes_out);
   s.shift = 4;
   while (s.shift < 8 && (pieces << s.shift) < chunks) s.shift++;
   return s;
@@ -425,7 +426,8 @@ ec_status ec_expert_dispatch(const void* x, int type, uint64_t tokens, uint64_t 
   if (!fine(x, type_bytes(type)) || !fine(xs, type_bytes(type)) || !fine(place, 4) ||
       !fine(offsets, 4))
     return EC_ERR_INVALID;
-  const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2);
+  const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
+                           tokens * choices * cols * type_bytes(type));
   BY_TYPE(type, hipLaunchKernelGGL((expert_dispatch<T>), dim3((uint32_t)blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)x, s, place,
                                    offsets, experts, (T*)xs));
@@ -441,7 +443,8 @@ ec_status ec_expert_dispatch_mx(const void* x, int type, uint64_t tokens, uint64
   if (!fine(x, type_bytes(type)) || !fine(codes, 16) || !fine(scales, 16) || !fine(place, 4) ||
       !fine(offsets, 4))
     return EC_ERR_INVALID;
-  const Shape s = shape_of(tokens, cols, choices, (uint32_t)(ec_mx_padded(cols) / 8), 2);
+  const Shape s = shape_of(tokens, cols, choices, (uint32_t)(ec_mx_padded(cols) / 8), 2,
+                           0);
   BY_TYPE(type, hipLaunchKernelGGL((expert_dispatch_mx<T>), dim3((uint32_t)blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)x, s, place,
                                    offsets, experts, (uint8_t*)codes, (uint8_t*)scales));
@@ -455,7 +458,8 @@ ec_status ec_expert_dispatch_backward(const void* dxs, int type, uint64_t tokens
   if (st != EC_OK || tokens == 0) return st;
   if (!fine(dxs, type_bytes(type)) || !fine(dx, type_bytes(type)) || !fine(place, 4))
     return EC_ERR_INVALID;
-  const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2);
+  const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
+                           tokens * cols * type_bytes(type));
   BY_TYPE(type, hipLaunchKernelGGL((expert_gather<T, false>), dim3((uint32_t)blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)dxs, s, place,
                                    (const void*)nullptr, 0, (T*)dx));
@@ -472,7 +476,8 @@ ec_status ec_expert_combine(const void* ys, int type, uint64_t tokens, uint64_t 
   if (!fine(ys, type_bytes(type)) || !fine(y, type_bytes(type)) || !fine(place, 4) ||
       !fine(weights, type_bytes(wtype)))
     return EC_ERR_INVALID;
-  const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2);
+  const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
+                           tokens * cols * type_bytes(type));
   BY_TYPE(type, hipLaunchKernelGGL((expert_gather<T, true>), dim3((uint32_t)blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)ys, s, place,
                                    weights, wtype, (T*)y));
@@ -492,7 +497,8 @@ ec_status ec_expert_combine_backward(const void* dy, const void* ys, int type, u
   if (!fine(dy, b) || !fine(ys, b) || !fine(dys, b) || !fine(place, 4) || !fine(offsets, 4) ||
       !fine(weights, wb) || !fine(dweights, wb))
     return EC_ERR_INVALID;
-  const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2);
+  const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
+                           tokens * choices * cols * b);
   BY_TYPE(type, hipLaunchKernelGGL((expert_combine_back<T, 2>), dim3((uint32_t)blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)dy,
                                    (const T*)ys, s, place, weights, wtype, offsets, experts,

@@ -50,6 +50,16 @@ __global__ __launch_bounds__(kThreads) void mx_rows(const T* __restrict__ x, uin
 
 // ---------------------------------------------------------------- rows and columns
 
+// The 16 bytes without their first n (n < 16, even), zeros behind.
+__device__ __forceinline__ void drop_bytes(uint32_t (&v)[4], uint32_t n) {
+  if (n & 8) v[0] = v[2], v[1] = v[3], v[2] = 0, v[3] = 0;
+  if (n & 4) v[0] = v[1], v[1] = v[2], v[2] = v[3], v[3] = 0;
+  if (n & 2) {
+    v[0] = v[0] >> 16 | v[1] << 16, v[1] = v[1] >> 16 | v[2] << 16;
+    v[2] = v[2] >> 16 | v[3] << 16, v[3] = v[3] >> 16;
+  }
+}
+
 // A wave takes 128 rows by 16 lanes of 16 bytes, a lane 32 rows of its 16
 // bytes, all in registers (128 of them): the blocks of its columns are then
 // its own, their magnitudes and codes need no exchange, and x is read once for
@@ -84,6 +94,26 @@ __global__ __launch_bounds__(kThreads, 2) void mx_both(
   if (c0 + E <= cols && r0 + 32 <= last) {
 #pragma unroll
     for (int i = 0; i < 32; i++) __builtin_memcpy(v[i], x + (r0 + i) * stride + c0, 16);
+  } else if (cols >= (uint32_t)E) {
+    // An end of the rows or columns: whole pieces from inside the array, the
+    // last one of a row from E elements before its end and moved down.
+    const uint32_t c = min(c0, cols - E);
+    const uint32_t past = (c0 - c) * sizeof(T);  // bytes to drop; 16 and more: all
+    const T* from = x + min(r0, last - 1) * stride + c;
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+      __builtin_memcpy(v[i], from, 16);
+      from += r0 + i + 1 < last ? stride : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+      const bool none = r0 + i >= last || past >= 16;
+      drop_bytes(v[i], past);
+#pragma unroll
+      for (int j = 0; j < 4; j++) v[i][j] = none ? 0 : v[i][j];
+      // kept here: moved to the uses, it would take registers for both forms
+      asm volatile("" : "+v"(v[i][0]), "+v"(v[i][1]), "+v"(v[i][2]), "+v"(v[i][3]));
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 32; i++) {
@@ -189,25 +219,30 @@ __device__ __forceinline__ void two_values(uint32_t* to, uint32_t c, float f) {
   }
 }
 
+// A lane makes 16 bytes of a row, so that a wave's stores have no gaps.
 template <typename T, int ROWS>
 __global__ __launch_bounds__(kThreads) void mx_values(const uint8_t* __restrict__ codes,
                                                       const uint8_t* __restrict__ scales,
                                                       uint64_t rows, uint32_t cols,
                                                       uint32_t padded, T* y, uint64_t stride,
-                                                      uint32_t tx_shift, uint32_t col_tiles) {
+                                                      uint32_t tx_shift, uint32_t col_tiles,
+                                                      bool past) {
+  constexpr uint32_t E = 16 / sizeof(T);
   const uint32_t tid = threadIdx.x, ty = kThreads >> tx_shift;
   const uint32_t ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;
-  const uint32_t chunk = (ct << tx_shift) + (tid & ((1u << tx_shift) - 1));
+  const uint32_t c0 = ((ct << tx_shift) + (tid & ((1u << tx_shift) - 1))) * E;
   const uint64_t row0 = (uint64_t)rt * ty * ROWS + (tid >> tx_shift);
-  if (chunk * 8 >= cols) return;
+  if (c0 >= cols) return;
   uint32_t c[ROWS], s[ROWS];
 #pragma unroll
   for (int i = 0; i < ROWS; i++) {
     const uint64_t row = row0 + (uint64_t)i * ty;
     c[i] = 0, s[i] = 0;
     if (row < rows) {
-      c[i] = *reinterpret_cast<const uint32_t*>(codes + row * (padded / 2) + chunk * 4);
-      s[i] = scales[row * (padded / 32) + chunk / 4];
+      const uint8_t* from = codes + row * (padded / 2) + c0 / 2;
+      c[i] = E == 8 ? *reinterpret_cast<const uint32_t*>(from)
+                    : *reinterpret_cast<const uint16_t*>(from);
+      s[i] = scales[row * (padded / 32) + c0 / 32];
     }
   }
 #pragma unroll
@@ -215,17 +250,29 @@ __global__ __launch_bounds__(kThreads) void mx_values(const uint8_t* __restrict_
     const uint64_t row = row0 + (uint64_t)i * ty;
     if (row >= rows) continue;
     const float f = bits_as<float>(s[i] == 0 ? 0x00400000u : s[i] << 23);
-    Eight<T> v;
-    two_values<T, 0>(v.w, c[i], f);
-    two_values<T, 1>(v.w, c[i], f);
-    two_values<T, 2>(v.w, c[i], f);
-    two_values<T, 3>(v.w, c[i], f);
+    uint32_t v[4];
+    two_values<T, 0>(v, c[i], f);
+    two_values<T, 1>(v, c[i], f);
+    if constexpr (E == 8) {
+      two_values<T, 2>(v, c[i], f);
+      two_values<T, 3>(v, c[i], f);
+    }
     if (s[i] == 255) {  // a block that is not finite
 #pragma unroll
-      for (int q = 0; q < Eight<T>::kWords; q++)
-        v.w[q] = sizeof(T) == 4 ? 0x7fc00000u : __is_same(T, bf16_t) ? 0x7fc07fc0u : 0x7e007e00u;
+      for (int q = 0; q < 4; q++)
+        v[q] = sizeof(T) == 4 ? 0x7fc00000u : __is_same(T, bf16_t) ? 0x7fc07fc0u : 0x7e007e00u;
     }
-    store_eight(y + row * stride + chunk * 8, (int64_t)cols - chunk * 8, v);
+    T* to = y + row * stride + c0;
+    if (c0 + E <= cols) {
+      if (past) store16_past(to, v);
+      else __builtin_memcpy(to, v, 16);
+    } else {
+      T e[E];
+      __builtin_memcpy(e, v, 16);
+#pragma unroll
+      for (uint32_t j = 0; j < E; j++)
+        if (c0 + j < cols) to[j] = e[j];
+    }
   }
 }
 
@@ -292,19 +339,21 @@ ec_status both_of(const void* x, uint64_t batch, uint64_t rows, uint64_t cols,
 template <typename T>
 ec_status values_of(const void* codes, const void* scales, uint64_t rows, uint64_t cols, void* y,
                     uint64_t stride, hipStream_t s) {
-  const uint32_t padded = (uint32_t)ec_mx_padded(cols), sh = lanes_shift(ceil_div(cols, 8));
-  const uint64_t tiles = ceil_div(ceil_div(cols, 8), 1ull << sh), ty = kThreads >> sh;
-  const uint32_t per = many(rows * (padded / 8)) ? 4 : 1;
+  const uint32_t padded = (uint32_t)ec_mx_padded(cols), E = 16 / sizeof(T);
+  const uint32_t sh = lanes_shift(ceil_div(cols, E));
+  const uint64_t tiles = ceil_div(ceil_div(cols, E), 1ull << sh), ty = kThreads >> sh;
+  const uint32_t per = many(rows * (padded / E)) ? 4 : 1;
   const uint64_t blocks = tiles * ceil_div(rows, ty * per);
   if (blocks > 0x7fffffffull) return EC_ERR_UNSUPPORTED;
+  const bool past = past_caches(rows * cols * sizeof(T));
   if (per == 4)
     hipLaunchKernelGGL((mx_values<T, 4>), dim3((uint32_t)blocks), dim3(kThreads), 0, s,
                        (const uint8_t*)codes, (const uint8_t*)scales, rows, (uint32_t)cols, padded,
-                       (T*)y, stride, sh, (uint32_t)tiles);
+                       (T*)y, stride, sh, (uint32_t)tiles, past);
   else
     hipLaunchKernelGGL((mx_values<T, 1>), dim3((uint32_t)blocks), dim3(kThreads), 0, s,
                        (const uint8_t*)codes, (const uint8_t*)scales, rows, (uint32_t)cols, padded,
-                       (T*)y, stride, sh, (uint32_t)tiles);
+                       (T*)y, stride, sh, (uint32_t)tiles, past);
   return launched();
 }
 

@@ -55,10 +55,29 @@ __device__ __forceinline__ Eight<T> load_eight(const T* p, int64_t n) {
   return v;
 }
 
+// Outputs that the 8 L2 caches of 4 MiB cannot hold are stored past them
+// (`past`): lines that wait there only to be written back cost the reads.
+inline bool past_caches(uint64_t bytes) { return bytes > (32ull << 20); }
+
+// 16 bytes to an address with the alignment of an element.
 template <typename T>
-__device__ __forceinline__ void store_eight(T* p, int64_t n, const Eight<T>& v) {
+__device__ __forceinline__ void store16_past(T* p, const void* v) {
+  typedef int unaligned __attribute__((ext_vector_type(4), aligned(2)));
+  unaligned w;
+  __builtin_memcpy(&w, v, 16);
+  __builtin_nontemporal_store(w, (unaligned*)p);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_eight(T* p, int64_t n, const Eight<T>& v,
+                                            bool past = false) {
   if (n >= 8) {
-    __builtin_memcpy(p, &v, sizeof(v));
+    // (two stores of a lane's 32 bytes leave gaps that only the caches close)
+    if (sizeof(T) == 2 && past) {
+      store16_past(p, v.w);
+    } else {
+      __builtin_memcpy(p, &v, sizeof(v));
+    }
   } else {
     T e[8];
     __builtin_memcpy(e, &v, sizeof(v));

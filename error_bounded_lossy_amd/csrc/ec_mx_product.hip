@@ -33,6 +33,7 @@ struct Product {
   uint32_t experts;
   uint32_t m_tiles, n_tiles;
   uint64_t tokens;   // kTokens: rows that the groups divide
+  bool past;         // stores go past the caches
 };
 
 // ---------------------------------------------------------------- tiles
@@ -384,7 +385,8 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx_tiles(const Produ
       if (m < m_end) {
         T* to = y + m * p.cols + nw + col;
         if (nw + col + kE <= p.cols) {
-          __builtin_memcpy(to, v, 16);
+          if (p.past) store16_past(to, v);
+          else __builtin_memcpy(to, v, 16);
         } else {
 #pragma unroll
           for (uint32_t u = 0; u < kE; u++)
@@ -544,6 +546,7 @@ ec_status tiles_as(Product p, hipStream_t s) {
   const uint64_t tiles = m * p.n_tiles * (MODE == kTokens ? p.experts : 1);
   if (tiles > 0x7ffffff0ull) return EC_ERR_UNSUPPORTED;
   p.m_tiles = (uint32_t)m;
+  p.past = past_caches(p.rows * p.cols * sizeof(T) * (MODE == kTokens ? p.experts : 1));
   hipLaunchKernelGGL((mx_tiles<FM, FN, T, MODE>), dim3((uint32_t)ceil_div(tiles, 8) * 8),
                      dim3(256), 0, s, p);
   return launched();
