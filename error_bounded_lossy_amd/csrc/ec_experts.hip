@@ -13,7 +13,7 @@ namespace {
 
 constexpr uint32_t kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 // ids of one workgroup's part; several parts count first and place after
-constexpr uint32_t kPart = 2048;
+constexpr uint32_t kPart = 1024;
 
 __device__ __forceinline__ uint32_t expert_of(const void* ids, uint32_t wide, uint64_t i,
                                               uint32_t experts) {
@@ -62,12 +62,25 @@ __global__ __launch_bounds__(kSortThreads) void expert_place(
   // thread e: this expert's choices in all parts, and in the parts before
   uint32_t all = 0, before = 0;
   if (counts) {
-    if (tid < cols)
-      for (uint32_t p = 0; p < parts; p++) {
+    // 16 loads at a time: a latency each would be most of this kernel's time
+    if (tid < cols) {
+      uint32_t p = 0;
+      for (; p + 16 <= parts; p += 16) {
+        uint32_t c[16];
+#pragma unroll
+        for (int i = 0; i < 16; i++) c[i] = counts[(uint64_t)(p + i) * cols + tid];
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+          before += p + i < blockIdx.x ? c[i] : 0;
+          all += c[i];
+        }
+      }
+      for (; p < parts; p++) {
         const uint32_t c = counts[(uint64_t)p * cols + tid];
         before += p < blockIdx.x ? c : 0;
         all += c;
       }
+    }
   } else {
     for (uint32_t e = tid; e < cols; e += kSortThreads) next[e] = 0;
     __syncthreads();
@@ -115,12 +128,14 @@ __global__ __launch_bounds__(kSortThreads) void expert_place(
     uint32_t to = 0;
     if (e < experts) {
       to = next[e] + rank;
-      for (uint32_t w = 0; w < wave; w++) to += ahead[w * experts + e];
+#pragma unroll
+      for (uint32_t w = 0; w < kSortWaves; w++) to += w < wave ? ahead[w * experts + e] : 0u;
     }
     if (i < last) {
       place[i] = e < experts ? (int32_t)to : -1;
       if (e < experts) order[to] = (int32_t)i;
     }
+    if (r + kSortThreads >= last) break;
     __syncthreads();
     for (uint32_t x = tid; x < experts; x += kSortThreads) {
       uint32_t c = 0;
@@ -215,13 +230,13 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch_mx(
   const uint64_t pitch = s.chunks * 4, spitch = s.chunks / 4;
   for (uint32_t c = a.lane; c < s.chunks; c += a.lanes) {
     const Eight<T> v = load_eight(x + a.token * s.cols + c * 8, (int64_t)s.cols - c * 8);
-    const uint32_t b = scale_byte(exponent_of<T>(max_of_4_lanes(magnitude_of_eight(v))));
-    const uint32_t code = code_eight(v, scale_of(b));
+    const Scale b = scale_of(exponent_of<T>(max_of_4_lanes(magnitude_of_eight(v))));
+    const uint32_t code = code_eight(v, b.size);
     for (uint32_t j = 0; j < s.choices; j++) {
       const int64_t r = row_of(place, s, a.token, j);
       if (r < 0) continue;
       *reinterpret_cast<uint32_t*>(codes + r * pitch + c * 4) = code;
-      if ((c & 3) == 0) scales[r * spitch + c / 4] = (uint8_t)b;
+      if ((c & 3) == 0) scales[r * spitch + c / 4] = (uint8_t)b.byte;
     }
   }
   for (uint64_t r = no_rows(offsets, experts, s.rows) + a.token; r < s.rows; r += s.tokens)
@@ -378,7 +393,7 @@ bool fine(const void* p, size_t to) { return p && aligned(p, to); }
 // parts of the sort: one where a workgroup does it all in a few rounds, else
 // up to 256, so that adding up the parts before stays short
 uint32_t sort_parts(uint64_t n) {
-  if (n <= 2 * kPart) return 1;
+  if (n <= 4 * kPart) return 1;
   const uint64_t p = ceil_div(n, kPart);
   return p > 256 ? 256 : (uint32_t)p;
 }

@@ -5,6 +5,8 @@
 // 17/32 of a byte, and a handful of instructions an element pair (the
 // magnitude is an integer maximum on packed patterns, the rounding one
 // conversion instruction for two elements).
+#include <type_traits>
+
 #include "ec_mx_device.h"
 
 using namespace ecmx;
@@ -39,11 +41,11 @@ __global__ __launch_bounds__(kThreads) void mx_rows(const T* __restrict__ x, uin
 #pragma unroll
   for (int i = 0; i < ROWS; i++) {
     const uint64_t row = row0 + (uint64_t)i * ty;
-    const uint32_t s = scale_byte(exponent_of<T>(max_of_4_lanes(magnitude_of_eight(v[i]))));
-    const uint32_t c = code_eight(v[i], scale_of(s));
+    const Scale s = scale_of(exponent_of<T>(max_of_4_lanes(magnitude_of_eight(v[i]))));
+    const uint32_t c = code_eight(v[i], s.size);
     if (row < rows) {
       *reinterpret_cast<uint32_t*>(codes + row * (padded / 2) + chunk * 4) = c;
-      if ((tid & 3) == 0) scales[row * (padded / 32) + chunk / 4] = (uint8_t)s;
+      if ((tid & 3) == 0) scales[row * (padded / 32) + chunk / 4] = (uint8_t)s.byte;
     }
   }
 }
@@ -111,53 +113,73 @@ __global__ __launch_bounds__(kThreads, 2) void mx_both(
       drop_bytes(v[i], past);
 #pragma unroll
       for (int j = 0; j < 4; j++) v[i][j] = none ? 0 : v[i][j];
-      // kept here: moved to the uses, it would take registers for both forms
       asm volatile("" : "+v"(v[i][0]), "+v"(v[i][1]), "+v"(v[i][2]), "+v"(v[i][3]));
     }
   } else {
+    // rows of less than 16 bytes: by elements, as whole words (as elements,
+    // the compiler would carry halves of words to the end of this kernel)
 #pragma unroll
-    for (int i = 0; i < 32; i++) {
-      T e[E];
+    for (int i = 0; i < 32; i++)
 #pragma unroll
-      for (int j = 0; j < E; j++)
-        e[j] = r0 + i < last && c0 + j < cols ? x[(r0 + i) * stride + c0 + j] : (T)0.0f;
-      __builtin_memcpy(v[i], e, 16);
-      // the row is put together here: its halves kept apart to the end of the
-      // loop would double the registers
-      asm volatile("" : "+v"(v[i][0]), "+v"(v[i][1]), "+v"(v[i][2]), "+v"(v[i][3]));
-    }
+      for (int j = 0; j < 4; j++) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int h = 0; h < 4 / (int)sizeof(T); h++) {
+          const uint32_t col = c0 + j * (4 / sizeof(T)) + h;
+          if (r0 + i < last && col < cols) {
+            const T* from = x + (r0 + i) * stride + col;
+            if constexpr (sizeof(T) == 4) w = *reinterpret_cast<const uint32_t*>(from);
+            else w |= (uint32_t) * reinterpret_cast<const uint16_t*>(from) << (16 * h);
+          }
+        }
+        v[i][j] = w;
+      }
   }
   if (ROWS && c0 < padded_cols) {
-    const uint64_t pitch = padded_cols / 2;
+    constexpr uint32_t kShare = 32 / E;  // lanes that share a block
+    const uint64_t pitch = padded_cols / 2, spitch = padded_cols / 32;
+    const uint32_t mine = lane & (kShare - 1);
     uint8_t* rc = row_codes + ((uint64_t)blockIdx.z * rows + r0) * pitch + c0 / 2;
-    uint8_t* rs = row_scales + ((uint64_t)blockIdx.z * rows + r0) * (padded_cols / 32) + c0 / 32;
+    uint8_t* rs = row_scales + ((uint64_t)blockIdx.z * rows + r0 + mine) * spitch + c0 / 32;
+    // Lanes that share a block store the scales of kShare rows in turn.  The
+    // checks of whole tiles are left out: without branches, the rows' chains
+    // of short operations overlap.
+    auto all_rows = [&](auto whole) {
 #pragma unroll
-    for (int i = 0; i < 32; i++) {
-      uint32_t m = magnitude<T>(v[i][0]);
+      for (int i0 = 0; i0 < 32; i0 += kShare) {
+        uint32_t byte = 0;
 #pragma unroll
-      for (int j = 1; j < 4; j++) m = larger<T>(m, magnitude<T>(v[i][j]));
-      m = joined<T>(m);
-      m = sizeof(T) == 4 ? max_of_8_lanes(m) : max_of_4_lanes(m);
-      const uint32_t s = scale_byte(exponent_of<T>(m));
-      const float f = scale_of(s);
-      uint32_t c = 0;
-      if constexpr (sizeof(T) == 4) {
-        c = code_two_f32<0>(c, v[i][0], v[i][1], f);
-        c = code_two_f32<1>(c, v[i][2], v[i][3], f);
-      } else {
-        c = code_two<T, 0>(c, v[i][0], f);
-        c = code_two<T, 1>(c, v[i][1], f);
-        c = code_two<T, 2>(c, v[i][2], f);
-        c = code_two<T, 3>(c, v[i][3], f);
+        for (int k = 0; k < (int)kShare; k++) {
+          const int i = i0 + k;
+          uint32_t m = magnitude<T>(v[i][0]);
+#pragma unroll
+          for (int j = 1; j < 4; j++) m = larger<T>(m, magnitude<T>(v[i][j]));
+          m = joined<T>(m);
+          m = sizeof(T) == 4 ? max_of_8_lanes(m) : max_of_4_lanes(m);
+          const Scale s = scale_of(exponent_of<T>(m));
+          byte = mine == (uint32_t)k ? s.byte : byte;
+          uint32_t c = 0;
+          if constexpr (sizeof(T) == 4) {
+            c = code_two_f32<0>(c, v[i][0], v[i][1], s.size);
+            c = code_two_f32<1>(c, v[i][2], v[i][3], s.size);
+          } else {
+            c = code_two<T, 0>(c, v[i][0], s.size);
+            c = code_two<T, 1>(c, v[i][1], s.size);
+            c = code_two<T, 2>(c, v[i][2], s.size);
+            c = code_two<T, 3>(c, v[i][3], s.size);
+          }
+          if (whole || r0 + i < last) {
+            if constexpr (sizeof(T) == 4)
+              *reinterpret_cast<uint16_t*>(rc + i * pitch) = (uint16_t)c;
+            else
+              *reinterpret_cast<uint32_t*>(rc + i * pitch) = c;
+          }
+        }
+        if (whole || r0 + i0 + mine < last) rs[i0 * spitch] = (uint8_t)byte;
       }
-      if (r0 + i < last) {
-        if constexpr (sizeof(T) == 4)
-          *reinterpret_cast<uint16_t*>(rc + i * pitch) = (uint16_t)c;
-        else
-          *reinterpret_cast<uint32_t*>(rc + i * pitch) = c;
-        if ((c0 & 31) == 0) rs[i * (uint64_t)(padded_cols / 32)] = (uint8_t)s;
-      }
-    }
+    };
+    if (first + 128 <= last) all_rows(std::true_type{});
+    else all_rows(std::false_type{});
   }
   if (COLS && c0 < cols) {
     uint32_t m[4];
@@ -174,8 +196,8 @@ __global__ __launch_bounds__(kThreads, 2) void mx_both(
     for (int j = 0; j < E; j++) {
       const int w = sizeof(T) == 4 ? j : j / 2, half = sizeof(T) == 4 ? 0 : j % 2;
       const uint32_t mj = sizeof(T) == 4 ? m[w] : (half ? m[w] >> 16 : m[w] & 0xffffu);
-      const uint32_t s = scale_byte(exponent_of<T>(mj));
-      const float f = scale_of(s);
+      const Scale s = scale_of(exponent_of<T>(mj));
+      const float f = s.size;
       uint32_t c[4] = {0, 0, 0, 0};
       // elements 2i and 2i + 1 of the column side by side: one byte permute
       auto pair = [&](int i) {
@@ -198,7 +220,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx_both(
       if (c0 + j < cols) {
         uint4 o = make_uint4(c[0], c[1], c[2], c[3]);
         *reinterpret_cast<uint4*>(cc + (uint64_t)j * (padded_rows / 2)) = o;
-        cs[(uint64_t)j * (padded_rows / 32)] = (uint8_t)s;
+        cs[(uint64_t)j * (padded_rows / 32)] = (uint8_t)s.byte;
       }
     }
   }

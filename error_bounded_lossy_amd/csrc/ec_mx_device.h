@@ -140,15 +140,17 @@ __device__ __forceinline__ uint32_t exponent_of(uint32_t m) {
   }
 }
 
-// The scale byte of a block whose largest magnitude has exponent field e.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t e) {
-  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
-}
-// The power of two that elements are divided by.  A block that is not finite
-// takes 2^126, so that its codes are defined; they read as NaN by its byte.
-__device__ __forceinline__ float scale_of(uint32_t s) {
-  const uint32_t t = s == 255u ? 253u : s;
-  return bits_as<float>(t == 0u ? 0x00400000u : t << 23);
+// A block's scale from the exponent field e of its largest magnitude: the
+// byte, and the power of two that elements are divided by, 2^-127 at least.
+// A block that is not finite takes 2^126, so that its codes are defined; they
+// read as NaN by its byte.
+struct Scale {
+  uint32_t byte;
+  float size;
+};
+__device__ __forceinline__ Scale scale_of(uint32_t e) {
+  const uint32_t s = __builtin_elementwise_sub_sat(e, 2u), bits = s << 23;
+  return {e == 255u ? 255u : s, bits_as<float>(bits > 0x00400000u ? bits : 0x00400000u)};
 }
 
 // Two elements into byte SEL of `old`.  The conversion instructions round to
@@ -206,6 +208,14 @@ __device__ __forceinline__ uint32_t max_of_8_lanes(uint32_t v) {
   v = max_of_4_lanes(v);
   const uint32_t t = __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true);  // mirrored in 8
   return v > t ? v : t;
+}
+
+// Consecutive workgroups go to the 8 XCDs in turn; with this, each XCD takes a
+// run of consecutive items instead.  The grid is `items` rounded up to 8.
+__device__ __forceinline__ bool dealt(uint32_t items, uint32_t& t) {
+  const uint32_t run = (items + 7) / 8;
+  t = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
+  return (blockIdx.x >> 3) < run && t < items;
 }
 
 // A group's rows, clamped to [0, rows] so that no offsets lead out of range.

@@ -146,15 +146,6 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("" ::: "memory");
 }
 
-// Tiles in the order that keeps the L2 caches useful: consecutive workgroups
-// go to the 8 XCDs in turn, so each XCD takes a run of consecutive tiles; in a
-// run, 8 tiles along the rows share a column tile.
-__device__ __forceinline__ bool tile_of(uint32_t tiles, uint32_t& t) {
-  const uint32_t run = (tiles + 7) / 8;
-  t = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
-  return (blockIdx.x >> 3) < run && t < tiles;
-}
-
 template <int FM, int FN, typename T, int MODE>
 __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx_tiles(const Product p) {
   constexpr int BM = 64 * FM, BN = 64 * FN, kWaves = 4;
@@ -171,12 +162,13 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx_tiles(const Produ
   uint32_t m_tiles = p.m_tiles;
   if (MODE == kExperts) m_tiles = min(m_tiles, used_tiles(p.offsets, p.experts, p.rows, kShift));
   uint32_t t;
-  if (!tile_of(m_tiles * p.n_tiles * (MODE == kTokens ? p.experts : 1), t)) return;
+  if (!dealt(m_tiles * p.n_tiles * (MODE == kTokens ? p.experts : 1), t)) return;
   uint32_t e = 0;
   if (MODE == kTokens) {
     e = t / (m_tiles * p.n_tiles);
     t -= e * (m_tiles * p.n_tiles);
   }
+  // in an XCD's run, 8 tiles along the rows share a column tile
   const uint32_t width = 8 * p.n_tiles, band = t / width;
   const uint32_t high = min(m_tiles - band * 8, 8u);
   uint32_t tm = band * 8 + (t - band * width) % high;
@@ -401,12 +393,15 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx_tiles(const Produ
 
 // ---------------------------------------------------------------- few rows
 
-// Up to 16 rows (of a group) at a time against 16 columns a workgroup: what
+// Up to 16 rows (of a group) at a time against 16 NT columns a workgroup: what
 // counts is reading b once, at full bandwidth.  The waves divide the
 // contraction in pieces of 512 elements; a lane loads 16 bytes of a row of b
 // and an instruction's 4 lanes of a row 64 bytes, straight into registers.
 // With x unquantized (T), the workgroup quantizes its rows into LDS first,
 // while the first loads of b are in flight.
+//
+// A wave keeps two loads of 4 KiB and more in flight: the pieces of two rounds
+// (SETS = 2) where it has several, else those of two column tiles (NT = 2).
 constexpr uint32_t kFewCols = 16, kFewRows = 16, kFewWaves = 8;
 constexpr uint32_t kPiece = 512;
 
@@ -430,15 +425,23 @@ struct Few {
   uint32_t held;  // rows that LDS holds (quantized here)
 };
 
-template <typename T, bool QUANTIZE>
-__global__ __launch_bounds__(64 * kFewWaves) void mx_few(const Few p) {
+// A piece of b: 4 steps of 128 elements, and their scale bytes, whole words
+// (a lane's byte is the one with its group's number).
+template <int NT>
+struct Piece {
+  i32x4 b[NT][4];
+  uint32_t s[NT][4];
+};
+
+template <typename T, bool QUANTIZE, int NT, int SETS>
+__global__ __launch_bounds__(64 * kFewWaves, 4) void mx_few(const Few p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ float part[kFewWaves][256];
+  __shared__ float part[kFewWaves][256 * NT];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t waves = blockDim.x >> 6;
   const uint32_t r = lane & 15, g = lane >> 4;
   const uint32_t tn = blockIdx.x % p.n_tiles, e = blockIdx.x / p.n_tiles;
-  const uint32_t n0 = tn * kFewCols;
+  const uint32_t n0 = tn * kFewCols * NT;
   uint64_t first = 0, count = p.rows;
   T* y = (T*)p.y;
   const uint8_t *bc = p.b.codes, *bs = p.b.scales;
@@ -446,10 +449,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_few(const Few p) {
     if (e == p.experts) {  // rows of no group: zeros
       int64_t f = p.offsets[p.experts];
       f = f < 0 ? 0 : f;
-      const uint32_t col = n0 + threadIdx.x % kFewCols;
+      const uint32_t col = n0 + threadIdx.x % (kFewCols * NT);
       if (col < p.cols)
-        for (uint64_t m = (uint64_t)f + threadIdx.x / kFewCols; m < p.rows;
-             m += blockDim.x / kFewCols)
+        for (uint64_t m = (uint64_t)f + threadIdx.x / (kFewCols * NT); m < p.rows;
+             m += blockDim.x / (kFewCols * NT))
           y[m * p.cols + col] = (T)0.0f;
       return;
     }
@@ -460,39 +463,63 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_few(const Few p) {
   }
   const uint32_t pitch = p.depth / 2, spitch = p.depth / 32;
   const uint32_t steps = p.depth / 128, pieces = (steps + 3) / 4;
-  const uint32_t n = min(n0 + r, p.cols - 1);
-  const uint8_t* gb = bc + (uint64_t)n * pitch + g * 16;
-  const uint8_t* gsb = bs + (uint64_t)n * spitch + g;
+  const uint8_t *gb[NT], *gsb[NT];
+#pragma unroll
+  for (int t = 0; t < NT; t++) {
+    const uint32_t n = min(n0 + t * kFewCols + r, p.cols - 1);
+    gb[t] = bc + (uint64_t)n * pitch + g * 16;
+    gsb[t] = bs + (uint64_t)n * spitch;
+  }
   const uint32_t lpitch = pitch + 16;  // rows of LDS start 4 banks apart
   uint8_t* lscales = lds + p.held * lpitch;
 
+  auto load = [&](Piece<NT>& f, uint32_t at) {
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+#pragma unroll
+      for (int s = 0; s < 4; s++)  // steps past the end read the last one
+        f.b[t][s] = *reinterpret_cast<const i32x4*>(gb[t] + min(at * 4 + s, steps - 1) * 64);
+      if (at * 4 + 4 <= steps) {
+        __builtin_memcpy(f.s[t], gsb[t] + at * 16, 16);
+      } else {
+#pragma unroll
+        for (int s = 0; s < 4; s++)
+          __builtin_memcpy(&f.s[t][s], gsb[t] + min(at * 4 + s, steps - 1) * 4, 4);
+      }
+    }
+  };
+
   for (uint64_t m0 = 0; m0 < count; m0 += QUANTIZE ? p.held : kFewRows) {
     const uint32_t here = (uint32_t)min((uint64_t)(QUANTIZE ? p.held : kFewRows), count - m0);
-    i32x4 fb[4];
-    int sb[4];
-    uint32_t piece = wave;
-    auto load = [&](uint32_t at) {
+    Piece<NT> f[SETS];
 #pragma unroll
-      for (int s = 0; s < 4; s++) {  // steps past the end read the last one
-        const uint32_t step = min(at * 4 + s, steps - 1);
-        fb[s] = *reinterpret_cast<const i32x4*>(gb + step * 64);
-        sb[s] = gsb[step * 4];
-      }
-    };
-    if (piece < pieces) load(piece);
+    for (int i = 0; i < SETS; i++)
+      if (wave + i * waves < pieces) load(f[i], wave + i * waves);
     const uint64_t row0 = first + m0;
     const uint32_t lr = min(r, here - 1);
     const uint8_t *ga, *gsa;
     if constexpr (QUANTIZE) {
-      const uint32_t chunks = p.depth / 8;
+      const uint32_t chunks = p.depth / 8, total = here * chunks;
       __syncthreads();  // the rows before are done
-      for (uint32_t i = threadIdx.x; i < here * chunks; i += blockDim.x) {
-        const uint32_t row = i / chunks, c = i - row * chunks;  // quads of lanes share a block
-        const Eight<T> v = load_eight((const T*)p.x + (row0 + row) * p.stride + c * 8,
-                                      (int64_t)p.raw_depth - c * 8);
-        const uint32_t s = scale_byte(exponent_of<T>(max_of_4_lanes(magnitude_of_eight(v))));
-        *reinterpret_cast<uint32_t*>(lds + row * lpitch + c * 4) = code_eight(v, scale_of(s));
-        if ((c & 3) == 0) lscales[row * spitch + c / 4] = (uint8_t)s;
+      constexpr int Q = 2;  // loads in flight; four cost spilled registers
+      for (uint32_t i0 = threadIdx.x; i0 < total; i0 += Q * blockDim.x) {
+        Eight<T> v[Q];
+        uint32_t row[Q], c[Q];
+#pragma unroll
+        for (int q = 0; q < Q; q++) {  // quads of lanes share a block
+          const uint32_t i = i0 + q * blockDim.x;
+          row[q] = i / chunks, c[q] = i - row[q] * chunks;
+          v[q] = load_eight((const T*)p.x + (row0 + row[q]) * p.stride + c[q] * 8,
+                            i < total ? (int64_t)p.raw_depth - c[q] * 8 : 0);
+        }
+#pragma unroll
+        for (int q = 0; q < Q; q++) {
+          if (i0 + q * blockDim.x >= total) break;
+          const Scale s = scale_of(exponent_of<T>(max_of_4_lanes(magnitude_of_eight(v[q]))));
+          *reinterpret_cast<uint32_t*>(lds + row[q] * lpitch + c[q] * 4) =
+              code_eight(v[q], s.size);
+          if ((c[q] & 3) == 0) lscales[row[q] * spitch + c[q] / 4] = (uint8_t)s.byte;
+        }
       }
       __syncthreads();
       ga = lds + lr * lpitch + g * 16;
@@ -501,33 +528,37 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_few(const Few p) {
       ga = p.a.codes + (row0 + lr) * pitch + g * 16;
       gsa = p.a.scales + (row0 + lr) * spitch + g;
     }
-    f32x4 acc = {};
-    while (piece < pieces) {
-      i32x4 wb[4];
-      int ws[4];
+    f32x4 acc[NT] = {};
+    for (uint32_t piece = wave; piece < pieces; piece += SETS * waves) {
 #pragma unroll
-      for (int s = 0; s < 4; s++) wb[s] = fb[s], ws[s] = sb[s];
-      const uint32_t now = piece;
-      piece += waves;
-      if (piece < pieces) load(piece);
+      for (int i = 0; i < SETS; i++) {
+        const uint32_t now = piece + i * waves;
+        if (now >= pieces) break;
 #pragma unroll
-      for (int s = 0; s < 4; s++) {
-        const uint32_t step = now * 4 + s;
-        if (step < steps) {
-          const i32x4 fa = *reinterpret_cast<const i32x4*>(ga + step * 64);
-          acc = multiply16(wb[s], fa, acc, ws[s], gsa[step * 4]);
+        for (int s = 0; s < 4; s++) {
+          const uint32_t step = now * 4 + s;
+          if (step < steps) {
+            const i32x4 fa = *reinterpret_cast<const i32x4*>(ga + step * 64);
+            const int sa = gsa[step * 4];
+#pragma unroll
+            for (int t = 0; t < NT; t++)
+              acc[t] = multiply16(f[i].b[t][s], fa, acc[t], (int)(f[i].s[t][s] >> (8 * g)), sa);
+          }
         }
+        if (now + SETS * waves < pieces) load(f[i], now + SETS * waves);
       }
     }
-    // a lane has row r of y and columns 4 g .. 4 g + 3; the waves' parts are
-    // added in their order
-    *reinterpret_cast<f32x4*>(&part[wave][r * 16 + g * 4]) = acc;
+    // a lane has row r of y and columns 4 g .. 4 g + 3 of a tile; the waves'
+    // parts are added in their order
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+      *reinterpret_cast<f32x4*>(&part[wave][(r * NT + t) * 16 + g * 4]) = acc[t];
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < here * 16; i += blockDim.x) {
+    for (uint32_t i = threadIdx.x; i < here * 16 * NT; i += blockDim.x) {
       float sum = 0;
       for (uint32_t w = 0; w < waves; w++) sum += part[w][i];
-      const uint32_t col = n0 + (i & 15);
-      if (col < p.cols) y[(row0 + (i >> 4)) * p.cols + col] = (T)sum;
+      const uint32_t col = n0 + i % (16 * NT);
+      if (col < p.cols) y[(row0 + i / (16 * NT)) * p.cols + col] = (T)sum;
     }
     if (m0 + (QUANTIZE ? p.held : kFewRows) < count) __syncthreads();
   }
@@ -572,18 +603,30 @@ ec_status tiles(const Product& p, int type, hipStream_t s) {
   }
 }
 
-template <typename T>
-ec_status few_of(const Few& p, bool quantize, hipStream_t s) {
+template <typename T, int NT, int SETS>
+ec_status few_as(Few p, bool quantize, uint32_t waves, hipStream_t s) {
+  p.n_tiles = (uint32_t)ceil_div(p.cols, kFewCols * NT);
   const uint64_t blocks = (uint64_t)p.n_tiles * (p.experts ? p.experts + 1 : 1);
   if (blocks > 0x7fffffffull) return EC_ERR_UNSUPPORTED;
-  const uint32_t pieces = (p.depth + kPiece - 1) / kPiece;
-  const uint32_t waves = pieces < kFewWaves ? pieces : kFewWaves;
   const uint32_t lds = quantize ? p.held * (p.depth / 2 + 16 + p.depth / 32) : 0;
   if (quantize)
-    hipLaunchKernelGGL((mx_few<T, true>), dim3((uint32_t)blocks), dim3(64 * waves), lds, s, p);
+    hipLaunchKernelGGL((mx_few<T, true, NT, SETS>), dim3((uint32_t)blocks), dim3(64 * waves), lds,
+                       s, p);
   else
-    hipLaunchKernelGGL((mx_few<T, false>), dim3((uint32_t)blocks), dim3(64 * waves), lds, s, p);
+    hipLaunchKernelGGL((mx_few<T, false, NT, SETS>), dim3((uint32_t)blocks), dim3(64 * waves), lds,
+                       s, p);
   return launched();
+}
+
+template <typename T>
+ec_status few_of(const Few& p, bool quantize, hipStream_t s) {
+  const uint32_t pieces = (p.depth + kPiece - 1) / kPiece;
+  const uint32_t waves = pieces < kFewWaves ? pieces : kFewWaves;
+  const uint64_t columns = (uint64_t)p.cols * (p.experts ? p.experts : 1);
+  // two column tiles where a wave has one piece and 512 workgroups remain
+  if (pieces <= kFewWaves && columns >= 512 * 2 * kFewCols)
+    return few_as<T, 2, 1>(p, quantize, waves, s);
+  return few_as<T, 1, 2>(p, quantize, waves, s);
 }
 
 ec_status few(const Few& p, int type, bool quantize, hipStream_t s) {
@@ -647,7 +690,6 @@ ec_status ec_mx_product(const void* a_codes, const void* a_scales, uint64_t rows
     f.a = {(const uint8_t*)a_codes, (const uint8_t*)a_scales};
     f.b = {(const uint8_t*)b_codes, (const uint8_t*)b_scales};
     f.y = y, f.rows = rows, f.cols = (uint32_t)cols, f.depth = (uint32_t)depth;
-    f.n_tiles = (uint32_t)ceil_div(cols, kFewCols);
     return few(f, type, false, (hipStream_t)stream);
   }
   Product p{};
@@ -672,7 +714,6 @@ ec_status ec_mx_product_experts(const void* a_codes, const void* a_scales, uint6
     f.b = {(const uint8_t*)b_codes, (const uint8_t*)b_scales};
     f.y = y, f.rows = rows, f.cols = (uint32_t)cols, f.depth = (uint32_t)depth;
     f.offsets = offsets, f.experts = experts;
-    f.n_tiles = (uint32_t)ceil_div(cols, kFewCols);
     return few(f, type, false, (hipStream_t)stream);
   }
   Product p{};
@@ -733,7 +774,6 @@ ec_status ec_mx_linear(const void* x, int type, uint64_t rows, uint64_t depth, u
     f.b = {(const uint8_t*)w_codes, (const uint8_t*)w_scales};
     f.y = y, f.rows = rows, f.cols = (uint32_t)cols, f.depth = (uint32_t)padded;
     f.offsets = offsets, f.experts = experts;
-    f.n_tiles = (uint32_t)ceil_div(cols, kFewCols);
     f.held = held_rows(rows, padded);
     return few(f, type, true, (hipStream_t)stream);
   }
