@@ -247,8 +247,9 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch_mx(
 }
 
 // y[t] = sum over the choices of w (or 1) times the choice's row, in fp32 and
-// in the choices' order; J rows are loaded before the first is added.
-template <typename T, bool WEIGHTED>
+// in the choices' order.  A lane has PIECES pieces of J rows in flight, and
+// places and weights are looked up once for all of them.
+template <typename T, bool WEIGHTED, int PIECES>
 __global__ __launch_bounds__(kThreads) void expert_gather(const T* __restrict__ ys, Shape s,
                                                           const int32_t* __restrict__ place,
                                                           const void* __restrict__ weights,
@@ -256,31 +257,44 @@ __global__ __launch_bounds__(kThreads) void expert_gather(const T* __restrict__ 
   constexpr int J = 4;
   const At a = at(s);
   if (a.token >= s.tokens) return;
-  for (uint32_t c = a.lane; c < s.chunks; c += a.lanes) {
-    const int64_t n = (int64_t)s.cols - c * 8;
-    float sum[8] = {};
+  for (uint32_t c0 = a.lane; c0 < s.chunks; c0 += a.lanes * PIECES) {
+    float sum[PIECES][8] = {};
     for (uint32_t j0 = 0; j0 < s.choices; j0 += J) {
-      Eight<T> v[J];
+      int64_t r[J];
       float w[J];
 #pragma unroll
-      for (int j = 0; j < J; j++) {
-        const int64_t r = j0 + j < s.choices ? row_of(place, s, a.token, j0 + j) : -1;
-        w[j] = 0;
-        v[j] = Eight<T>{};
-        if (r >= 0) {  // what a dropped choice's weight holds is not read
-          v[j] = load_eight(ys + r * s.cols + c * 8, n);
-          w[j] = WEIGHTED ? weight_at(weights, wtype, a.token * s.choices + j0 + j) : 1.0f;
+      for (int j = 0; j < J; j++)
+        r[j] = j0 + j < s.choices ? row_of(place, s, a.token, j0 + j) : -1;
+#pragma unroll
+      for (int j = 0; j < J; j++)  // what a dropped choice's weight holds is not read
+        w[j] = r[j] < 0 ? 0.0f
+               : WEIGHTED ? weight_at(weights, wtype, a.token * s.choices + j0 + j) : 1.0f;
+      Eight<T> v[PIECES][J];
+#pragma unroll
+      for (int j = 0; j < J; j++)
+#pragma unroll
+        for (int i = 0; i < PIECES; i++) {
+          const uint32_t c = c0 + i * a.lanes;
+          v[i][j] = load_eight(ys + r[j] * s.cols + (uint64_t)c * 8,
+                               r[j] >= 0 && c < s.chunks ? (int64_t)s.cols - (int64_t)c * 8 : 0);
         }
-      }
 #pragma unroll
-      for (int j = 0; j < J; j++) {
-        float f[8];
-        widen(v[j], f);
+      for (int i = 0; i < PIECES; i++)
 #pragma unroll
-        for (int i = 0; i < 8; i++) sum[i] += WEIGHTED ? w[j] * f[i] : f[i];
-      }
+        for (int j = 0; j < J; j++) {
+          float f[8];
+          widen(v[i][j], f);
+#pragma unroll
+          for (int q = 0; q < 8; q++) sum[i][q] += WEIGHTED ? w[j] * f[q] : f[q];
+        }
     }
-    store_eight(y + a.token * s.cols + c * 8, n, narrow<T>(sum), s.past);
+#pragma unroll
+    for (int i = 0; i < PIECES; i++) {
+      const uint32_t c = c0 + i * a.lanes;
+      if (c < s.chunks)
+        store_eight(y + a.token * s.cols + (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8,
+                    narrow<T>(sum[i]), s.past);
+    }
   }
 }
 
@@ -475,7 +489,7 @@ ec_status ec_expert_dispatch_backward(const void* dxs, int type, uint64_t tokens
     return EC_ERR_INVALID;
   const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
                            tokens * cols * type_bytes(type));
-  BY_TYPE(type, hipLaunchKernelGGL((expert_gather<T, false>), dim3((uint32_t)blocks_of(s)),
+  BY_TYPE(type, hipLaunchKernelGGL((expert_gather<T, false, 2>), dim3((uint32_t)blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)dxs, s, place,
                                    (const void*)nullptr, 0, (T*)dx));
   return launched();
@@ -493,7 +507,7 @@ ec_status ec_expert_combine(const void* ys, int type, uint64_t tokens, uint64_t 
     return EC_ERR_INVALID;
   const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
                            tokens * cols * type_bytes(type));
-  BY_TYPE(type, hipLaunchKernelGGL((expert_gather<T, true>), dim3((uint32_t)blocks_of(s)),
+  BY_TYPE(type, hipLaunchKernelGGL((expert_gather<T, true, 2>), dim3((uint32_t)blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)ys, s, place,
                                    weights, wtype, (T*)y));
   return launched();

@@ -211,11 +211,13 @@ __device__ __forceinline__ uint32_t max_of_8_lanes(uint32_t v) {
 }
 
 // Consecutive workgroups go to the 8 XCDs in turn; with this, each XCD takes a
-// run of consecutive items instead.  The grid is `items` rounded up to 8.
-__device__ __forceinline__ bool dealt(uint32_t items, uint32_t& t) {
-  const uint32_t run = (items + 7) / 8;
-  t = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
-  return (blockIdx.x >> 3) < run && t < items;
+// run of consecutive items, of each of `sets` sets in turn.  The grid is
+// `items` rounded up to 8, times sets.
+__device__ __forceinline__ bool dealt(uint32_t items, uint32_t sets, uint32_t& t, uint32_t& set) {
+  const uint32_t run = (items + 7) / 8, i = blockIdx.x >> 3;
+  set = i / run;
+  t = (blockIdx.x & 7) * run + (i - set * run);
+  return set < sets && t < items;
 }
 
 // A group's rows, clamped to [0, rows] so that no offsets lead out of range.

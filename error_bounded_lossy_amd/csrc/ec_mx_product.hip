@@ -161,13 +161,10 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx_tiles(const Produ
   // the tiles that groups have, not the most they could have: each XCD gets its share
   uint32_t m_tiles = p.m_tiles;
   if (MODE == kExperts) m_tiles = min(m_tiles, used_tiles(p.offsets, p.experts, p.rows, kShift));
-  uint32_t t;
-  if (!dealt(m_tiles * p.n_tiles * (MODE == kTokens ? p.experts : 1), t)) return;
-  uint32_t e = 0;
-  if (MODE == kTokens) {
-    e = t / (m_tiles * p.n_tiles);
-    t -= e * (m_tiles * p.n_tiles);
-  }
+  // (an expert's tiles cost what it has of tokens: each XCD gets a share of
+  // every expert, not some experts whole)
+  uint32_t t, e = 0;
+  if (!dealt(m_tiles * p.n_tiles, MODE == kTokens ? p.experts : 1, t, e)) return;
   // in an XCD's run, 8 tiles along the rows share a column tile
   const uint32_t width = 8 * p.n_tiles, band = t / width;
   const uint32_t high = min(m_tiles - band * 8, 8u);
@@ -574,23 +571,32 @@ ec_status tiles_as(Product p, hipStream_t s) {
   uint64_t m = ceil_div(p.rows, 64 * FM);
   // groups round up each, and the rows of no group once more
   if (MODE == kExperts) m += (p.experts < p.rows ? p.experts : p.rows) + 1;
-  const uint64_t tiles = m * p.n_tiles * (MODE == kTokens ? p.experts : 1);
-  if (tiles > 0x7ffffff0ull) return EC_ERR_UNSUPPORTED;
+  const uint64_t tiles = ceil_div(m * p.n_tiles, 8) * 8 * (MODE == kTokens ? p.experts : 1);
+  if (tiles > 0x7fffffffull) return EC_ERR_UNSUPPORTED;
   p.m_tiles = (uint32_t)m;
   p.past = past_caches(p.rows * p.cols * sizeof(T) * (MODE == kTokens ? p.experts : 1));
-  hipLaunchKernelGGL((mx_tiles<FM, FN, T, MODE>), dim3((uint32_t)ceil_div(tiles, 8) * 8),
+  hipLaunchKernelGGL((mx_tiles<FM, FN, T, MODE>), dim3((uint32_t)tiles),
                      dim3(256), 0, s, p);
   return launched();
 }
 
+// The larger tile reads less and keeps the matrix units busier, but the last
+// round of its workgroups (one a unit, 256 in all) may be nearly empty; of the
+// tiles of 128, two workgroups share a unit, and they cost 8% more for every
+// 1024 of the contraction (8192 x 8192 outputs: 78 against 73 us at 1024, 350
+// against 300 at 8192).  Rounds in units of the larger tile's, times 1024:
 template <typename T, int MODE>
 ec_status tiles_of(const Product& p, hipStream_t s) {
   const uint64_t groups = MODE == kTokens ? p.experts : 1;
-  // the larger tile reads less, as long as it leaves work for every unit
-  if (ceil_div(p.rows, 256) * ceil_div(p.cols, 256) * groups >= 192)
-    return tiles_as<4, 4, T, MODE>(p, s);
-  if (ceil_div(p.rows, 128) * ceil_div(p.cols, 128) * groups >= 128)
-    return tiles_as<2, 2, T, MODE>(p, s);
+  // rows of experts: half a tile more for each
+  const uint64_t extra = MODE == kExperts ? p.experts / 2 : 0;
+  const uint64_t large = (ceil_div(p.rows, 256) + extra) * ceil_div(p.cols, 256) * groups;
+  const uint64_t small = (ceil_div(p.rows, 128) + extra) * ceil_div(p.cols, 128) * groups;
+  const uint64_t depth = MODE == kTokens ? p.tokens / p.experts : p.depth;
+  const uint64_t cost_large = ceil_div(large, 256) * 1024;
+  const uint64_t cost_small = ceil_div(small, 512) * (512 + depth / 25);
+  if (large >= 192 && cost_large <= cost_small) return tiles_as<4, 4, T, MODE>(p, s);
+  if (small >= 128) return tiles_as<2, 2, T, MODE>(p, s);
   return tiles_as<1, 1, T, MODE>(p, s);
 }
 

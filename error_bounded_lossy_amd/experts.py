@@ -36,13 +36,12 @@ def expert_sort(ids: torch.Tensor, experts: int, stream=None) -> Routing:
         _refuse("expert_sort: a positive number of experts is wanted")
     if not ids.is_contiguous():
         ids = ids.contiguous()
-    n, device = ids.numel(), ids.device
-    order = torch.empty(n, dtype=torch.int32, device=device)
-    place = torch.empty(ids.shape, dtype=torch.int32, device=device)
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
+    n = ids.numel()
+    place = torch.empty_like(ids, dtype=torch.int32)
+    order, offsets = place.new_empty(n), place.new_empty(experts + 1)
     L = _b.lib()
     need = L.ec_expert_sort_workspace_bytes(n, experts)
-    ws = torch.empty(need, dtype=torch.uint8, device=device).data_ptr() if need else None
+    ws = place.new_empty(need, dtype=torch.uint8).data_ptr() if need else None
     _b.check(L.ec_expert_sort(ids.data_ptr(), ids.element_size(), n, experts, order.data_ptr(),
                               place.data_ptr(), offsets.data_ptr(), ws, need,
                               _b.current_stream(ids)), "ec_expert_sort")
@@ -79,7 +78,7 @@ def expert_dispatch(x: torch.Tensor, routing: Routing, stream=None) -> torch.Ten
     r = routing
     x, kind = _tokens(x, r, "expert_dispatch")
     cols = x.shape[1]
-    xs = torch.empty((r.tokens * r.choices, cols), dtype=x.dtype, device=x.device)
+    xs = x.new_empty((r.tokens * r.choices, cols))
     _b.check(_b.lib().ec_expert_dispatch(x.data_ptr(), kind, r.tokens, cols, r.place.data_ptr(),
                                          r.choices, r.offsets.data_ptr(), r.experts,
                                          xs.data_ptr(), _b.current_stream(x)),
@@ -94,7 +93,7 @@ def expert_dispatch_mx(x: torch.Tensor, routing: Routing, stream=None) -> MXTens
     r = routing
     x, kind = _tokens(x, r, "expert_dispatch_mx")
     cols = x.shape[1]
-    q = _empty((r.tokens * r.choices,), cols, x.device)
+    q = _empty((r.tokens * r.choices,), cols, x)
     _b.check(_b.lib().ec_expert_dispatch_mx(x.data_ptr(), kind, r.tokens, cols,
                                             r.place.data_ptr(), r.choices, r.offsets.data_ptr(),
                                             r.experts, q.codes.data_ptr(), q.scales.data_ptr(),
@@ -108,7 +107,7 @@ def expert_dispatch_backward(dxs: torch.Tensor, routing: Routing, stream=None) -
         return _b.on_stream(expert_dispatch_backward, (dxs, routing), stream)
     r = routing
     dxs, kind = _sorted(dxs, r, "expert_dispatch_backward")
-    dx = torch.empty((r.tokens, dxs.shape[1]), dtype=dxs.dtype, device=dxs.device)
+    dx = dxs.new_empty((r.tokens, dxs.shape[1]))
     _b.check(_b.lib().ec_expert_dispatch_backward(dxs.data_ptr(), kind, r.tokens, dxs.shape[1],
                                                   r.place.data_ptr(), r.choices, dx.data_ptr(),
                                                   _b.current_stream(dxs)),
@@ -124,7 +123,7 @@ def expert_combine(ys: torch.Tensor, routing: Routing, weights: torch.Tensor,
     r = routing
     ys, kind = _sorted(ys, r, "expert_combine")
     w, wkind = _weights(weights, r, "expert_combine")
-    y = torch.empty((r.tokens, ys.shape[1]), dtype=ys.dtype, device=ys.device)
+    y = ys.new_empty((r.tokens, ys.shape[1]))
     _b.check(_b.lib().ec_expert_combine(ys.data_ptr(), kind, r.tokens, ys.shape[1],
                                         r.place.data_ptr(), r.choices, w.data_ptr(), wkind,
                                         y.data_ptr(), _b.current_stream(ys)), "ec_expert_combine")

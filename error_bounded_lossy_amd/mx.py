@@ -74,10 +74,10 @@ def _made(codes, scales, cols) -> MXTensor:
     return m
 
 
-def _empty(lead, cols, device, p=None) -> MXTensor:
+def _empty(lead, cols, like, p=None) -> MXTensor:
     p = (cols + 127) // 128 * 128 if p is None else p
-    return _made(torch.empty((*lead, p // 2), dtype=torch.uint8, device=device),
-                 torch.empty((*lead, p // 32), dtype=torch.uint8, device=device), cols)
+    codes = like.new_empty((*lead, p // 2), dtype=torch.uint8)
+    return _made(codes, codes.new_empty((*lead, p // 32)), cols)
 
 
 def mx_quantize(x: torch.Tensor, stream=None) -> MXTensor:
@@ -88,7 +88,7 @@ def mx_quantize(x: torch.Tensor, stream=None) -> MXTensor:
     if x.dim() == 0 or x.shape[-1] == 0:
         _refuse("mx_quantize: at least one element a row is wanted")
     r = _rows(x)
-    q = _empty(x.shape[:-1], x.shape[-1], x.device)
+    q = _empty(x.shape[:-1], x.shape[-1], x)
     _b.check(_b.lib().ec_mx_quantize(r.data_ptr(), kind, r.shape[0], r.shape[1], r.stride(0),
                                      q.codes.data_ptr(), q.scales.data_ptr(),
                                      _b.current_stream(x)), "ec_mx_quantize")
@@ -108,7 +108,7 @@ def mx_quantize_both(x: torch.Tensor, stream=None) -> tuple[MXTensor, MXTensor]:
         x = x.contiguous()
     lead = x.shape[:-2]
     batch = x.shape[0] if x.dim() == 3 else 1
-    a, b = _empty((*lead, rows), cols, x.device), _empty((*lead, cols), rows, x.device)
+    a, b = _empty((*lead, rows), cols, x), _empty((*lead, cols), rows, x)
     if rows and batch:
         _b.check(_b.lib().ec_mx_quantize_both(
             x.data_ptr(), kind, batch, rows, cols, x.stride(0) if x.dim() == 3 else 0, x.stride(-2),
@@ -125,7 +125,7 @@ def mx_dequantize(q: MXTensor, dtype: torch.dtype = torch.float32, stream=None) 
     if kind is None or not q.codes.is_cuda or q.cols == 0:
         _refuse("mx_dequantize: a nonempty row on the GPU and float32, float16 or bfloat16 are wanted")
     lead = q.codes.shape[:-1]
-    y = torch.empty((*lead, q.cols), dtype=dtype, device=q.codes.device)
+    y = q.codes.new_empty((*lead, q.cols), dtype=dtype)
     rows = y.numel() // q.cols
     _b.check(_b.lib().ec_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), rows, q.cols,
                                        y.data_ptr(), kind, q.cols, _b.current_stream(y)),
@@ -166,9 +166,9 @@ def _linear(x, w, offsets, experts, what):
     r = _rows(x)
     rows = r.shape[0]
     L = _b.lib()
-    y = torch.empty((*x.shape[:-1], cols), dtype=x.dtype, device=x.device)
+    y = x.new_empty((*x.shape[:-1], cols))
     need = L.ec_mx_linear_workspace_bytes(rows, depth, cols, experts)
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device).data_ptr() if need else None
+    ws = w.codes.new_empty(need).data_ptr() if need else None
     _b.check(L.ec_mx_linear(r.data_ptr(), kind, rows, depth, r.stride(0), w.codes.data_ptr(),
                             w.scales.data_ptr(), cols,
                             offsets.data_ptr() if experts else None, experts, y.data_ptr(), ws,
@@ -238,8 +238,8 @@ def _quantize_groups(x, offsets, experts, rows_too=True):
     r = x if x.stride(1) == 1 and x.stride(0) >= x.shape[1] else x.contiguous()
     rows, cols = x.shape
     L = _b.lib()
-    a = _empty((rows,), cols, x.device)
-    b = _empty((cols,), rows, x.device, int(L.ec_mx_padded_groups(rows, experts)))
+    a = _empty((rows,), cols, x)
+    b = _empty((cols,), rows, x, int(L.ec_mx_padded_groups(rows, experts)))
     if rows:
         _b.check(L.ec_mx_quantize_groups(r.data_ptr(), TYPES[x.dtype], rows, cols, r.stride(0),
                                          offsets.data_ptr(), experts, a.codes.data_ptr(),

@@ -294,6 +294,18 @@ def test_experts_large_tiles(dtype):
     assert not y[sum(counts):].any() and not dx[sum(counts):].any() and not dw[1].any()
 
 
+def test_experts_tiles_of_256():
+    # enough rows and columns for the largest tile, in one round of workgroups
+    counts = [2000, 1, 0, 1700, 300]
+    x, offsets = grouped(counts, 60, 1, 384, torch.bfloat16)
+    w = activations(2, 5, 3001, 384, spread=1.0)
+    y = ec.mx_experts_linear(x, ec.mx_quantize(w), offsets)
+    for e, (a, b) in enumerate(parts(offsets)):
+        if a < b:
+            R.check(y[a:b], *R.mm_bound(R.near(x[a:b]), R.near(w[e]), torch.bfloat16), f"y {e}")
+    assert not y[sum(counts):].any()
+
+
 @pytest.mark.parametrize("offsets", [[0, 50, 20, 90], [-5, 10, 400, 90], [70, 70, 10, 0], [0, 0, 0, 500]],
                          ids=str)
 def test_offsets_out_of_order_stay_in_bounds(offsets):
