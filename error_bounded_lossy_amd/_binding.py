@@ -19,12 +19,13 @@ def check(status: int, what: str):
 def current_stream(t: torch.Tensor) -> int:
     """The handle of torch's current stream on t's device (the raw getter: a Stream object costs
     more than a small call's launch)."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def elsewhere(t: torch.Tensor) -> bool:
     """Whether t lies on a GPU that is not the current one."""
-    return t.is_cuda and t.device.index != torch._C._cuda_getDevice()
+    device = t.get_device()  # -1: not on a GPU
+    return device >= 0 and device != torch._C._cuda_getDevice()
 
 
 def _tensors(v):

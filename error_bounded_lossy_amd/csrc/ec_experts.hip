@@ -265,10 +265,14 @@ __global__ __launch_bounds__(kThreads) void expert_gather(const T* __restrict__ 
 #pragma unroll
       for (int j = 0; j < J; j++)
         r[j] = j0 + j < s.choices ? row_of(place, s, a.token, j0 + j) : -1;
+      if (WEIGHTED) {
+        const uint64_t at = a.token * s.choices + j0;
 #pragma unroll
-      for (int j = 0; j < J; j++)  // what a dropped choice's weight holds is not read
-        w[j] = r[j] < 0 ? 0.0f
-               : WEIGHTED ? weight_at(weights, wtype, a.token * s.choices + j0 + j) : 1.0f;
+        for (int j = 0; j < J; j++) {  // a dropped choice's weight may hold anything
+          w[j] = weight_at(weights, wtype, at + (j0 + j < s.choices ? j : 0));
+          w[j] = r[j] < 0 ? 0.0f : w[j];
+        }
+      }
       Eight<T> v[PIECES][J];
 #pragma unroll
       for (int j = 0; j < J; j++)

@@ -28,11 +28,16 @@ def _type(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def _rows(x: torch.Tensor) -> torch.Tensor:
-    """x as [rows, cols] with unit column stride (a copy only where its strides allow no view)."""
+def _rows(x: torch.Tensor) -> tuple[torch.Tensor, int]:
+    """x as [rows, cols] with unit column stride, and its row stride (a copy only where its strides
+    allow no view).  Strides of sizes of one hold anything: those of contiguous rows are not read."""
     if x.dim() != 2:
         x = x.reshape(-1, x.shape[-1])
-    return x if x.stride(1) == 1 and x.stride(0) >= x.shape[1] else x.contiguous()
+    if not x.is_contiguous():
+        if x.stride(1) == 1 and x.stride(0) >= x.shape[1]:
+            return x, x.stride(0)
+        x = x.contiguous()
+    return x, x.shape[1]
 
 
 def padded(cols: int) -> int:
@@ -87,9 +92,9 @@ def mx_quantize(x: torch.Tensor, stream=None) -> MXTensor:
     kind = _type(x, "mx_quantize")
     if x.dim() == 0 or x.shape[-1] == 0:
         _refuse("mx_quantize: at least one element a row is wanted")
-    r = _rows(x)
+    r, stride = _rows(x)
     q = _empty(x.shape[:-1], x.shape[-1], x)
-    _b.check(_b.lib().ec_mx_quantize(r.data_ptr(), kind, r.shape[0], r.shape[1], r.stride(0),
+    _b.check(_b.lib().ec_mx_quantize(r.data_ptr(), kind, r.shape[0], r.shape[1], stride,
                                      q.codes.data_ptr(), q.scales.data_ptr(),
                                      _b.current_stream(x)), "ec_mx_quantize")
     return q
@@ -104,14 +109,17 @@ def mx_quantize_both(x: torch.Tensor, stream=None) -> tuple[MXTensor, MXTensor]:
     if x.dim() not in (2, 3) or x.shape[-1] == 0:
         _refuse("mx_quantize_both: [rows, cols] or [batch, rows, cols] is wanted")
     rows, cols = x.shape[-2:]
-    if x.stride(-1) != 1 or x.stride(-2) < cols or (x.dim() == 3 and x.stride(0) < 0):
+    if not x.is_contiguous() and (x.stride(-1) != 1 or x.stride(-2) < cols):
         x = x.contiguous()
+    stride, batch_stride = cols, rows * cols
+    if not x.is_contiguous():
+        stride, batch_stride = x.stride(-2), x.stride(0)
     lead = x.shape[:-2]
     batch = x.shape[0] if x.dim() == 3 else 1
     a, b = _empty((*lead, rows), cols, x), _empty((*lead, cols), rows, x)
     if rows and batch:
         _b.check(_b.lib().ec_mx_quantize_both(
-            x.data_ptr(), kind, batch, rows, cols, x.stride(0) if x.dim() == 3 else 0, x.stride(-2),
+            x.data_ptr(), kind, batch, rows, cols, batch_stride, stride,
             a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
             _b.current_stream(x)), "ec_mx_quantize_both")
     return a, b
@@ -163,13 +171,13 @@ def _linear(x, w, offsets, experts, what):
     cols, depth = w.codes.shape[-2], x.shape[-1]
     if w.cols != depth or depth == 0 or w.codes.device != x.device:
         _refuse(f"{what}: weights [.., cols, depth] on the device of x [.., depth] are wanted")
-    r = _rows(x)
+    r, stride = _rows(x)
     rows = r.shape[0]
     L = _b.lib()
     y = x.new_empty((*x.shape[:-1], cols))
     need = L.ec_mx_linear_workspace_bytes(rows, depth, cols, experts)
     ws = w.codes.new_empty(need).data_ptr() if need else None
-    _b.check(L.ec_mx_linear(r.data_ptr(), kind, rows, depth, r.stride(0), w.codes.data_ptr(),
+    _b.check(L.ec_mx_linear(r.data_ptr(), kind, rows, depth, stride, w.codes.data_ptr(),
                             w.scales.data_ptr(), cols,
                             offsets.data_ptr() if experts else None, experts, y.data_ptr(), ws,
                             need, _b.current_stream(x)), "ec_mx_linear")
@@ -235,13 +243,13 @@ def mx_linear_backward(dy: torch.Tensor, saved: MXLinearSaved, stream=None):
 
 
 def _quantize_groups(x, offsets, experts, rows_too=True):
-    r = x if x.stride(1) == 1 and x.stride(0) >= x.shape[1] else x.contiguous()
+    r, stride = _rows(x)
     rows, cols = x.shape
     L = _b.lib()
     a = _empty((rows,), cols, x)
     b = _empty((cols,), rows, x, int(L.ec_mx_padded_groups(rows, experts)))
     if rows:
-        _b.check(L.ec_mx_quantize_groups(r.data_ptr(), TYPES[x.dtype], rows, cols, r.stride(0),
+        _b.check(L.ec_mx_quantize_groups(r.data_ptr(), TYPES[x.dtype], rows, cols, stride,
                                          offsets.data_ptr(), experts, a.codes.data_ptr(),
                                          a.scales.data_ptr(), b.codes.data_ptr(),
                                          b.scales.data_ptr(), _b.current_stream(x)),

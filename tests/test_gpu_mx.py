@@ -116,6 +116,23 @@ def test_strides_and_alignment(dtype):
     same_form(ec.mx_quantize_both(batch)[1], batch.transpose(1, 2))
 
 
+def test_strides_of_sizes_of_one():
+    # a single row or column: its stride may be anything, here 1
+    row = activations(1, 200, 1).t()
+    assert row.shape == (1, 200) and row.stride(0) == 1
+    w = ec.mx_quantize(activations(2, 30, 200))
+    want, bound = R.mm_bound(R.near(row), ec.mx_dequantize(w, torch.float32).double(), torch.bfloat16)
+    R.check(ec.mx_linear(row, w), want, bound)
+    offsets = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    y, saved = ec.mx_experts_forward(row, activations(3, 1, 30, 200), offsets)
+    assert y.shape == (1, 30) and ec.mx_experts_backward(y, saved)[0].shape == (1, 200)
+    for x in (row, row.t(), row.unsqueeze(0), row.t().unsqueeze(0), activations(4, 5, 7, 1).transpose(0, 2)):
+        same_form(ec.mx_quantize(x), x)
+        a, b = ec.mx_quantize_both(x)
+        same_form(a, x)
+        same_form(b, x.transpose(-1, -2))
+
+
 def test_empty_rows_and_leading_dimensions():
     x = activations(1, 2, 3, 40)
     same_form(ec.mx_quantize(x), x)
