@@ -526,7 +526,7 @@ class Huffman:
 # --- the 4-bit format and the token exchange (include/ec_mx.h, ec_experts.h) -
 _OPERATORS = {
     "mx": ("MXTensor", "MXLinearSaved", "mx_quantize", "mx_quantize_both", "mx_dequantize",
-           "mx_product", "mx_linear", "mx_experts_linear", "mx_linear_forward",
+           "mx_product", "mx_linear", "mx_experts_linear", "mx_experts_product", "mx_linear_forward",
            "mx_linear_backward", "mx_experts_forward", "mx_experts_backward"),
     "experts": ("Routing", "expert_sort", "expert_dispatch", "expert_dispatch_mx",
                 "expert_dispatch_backward", "expert_combine", "expert_combine_backward"),

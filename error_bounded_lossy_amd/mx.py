@@ -206,6 +206,20 @@ def mx_experts_linear(x: torch.Tensor, w: MXTensor, offsets: torch.Tensor,
     return _linear(x, w, offsets, experts, "mx_experts_linear")
 
 
+def mx_experts_product(a: MXTensor, b: MXTensor, offsets: torch.Tensor,
+                       dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """mx_experts_linear of rows that are in the 4-bit form already, as expert_dispatch_mx makes
+    them: a [rows, depth], b [experts, cols, depth]."""
+    if stream is not None or _b.elsewhere(a.codes):
+        return _b.on_stream(mx_experts_product, (a, b, offsets, dtype), stream)
+    if (dtype not in TYPES or a.codes.dim() != 2 or b.codes.dim() != 3 or a.cols != b.cols
+            or a.cols == 0 or 0 in b.codes.shape or not a.codes.is_cuda
+            or a.codes.device != b.codes.device):
+        _refuse("mx_experts_product: [rows, depth] and [experts, cols, depth] on one GPU are wanted")
+    _offsets(offsets, b.codes.shape[0], a.codes.device, "mx_experts_product")
+    return _experts_product(a, b, offsets, dtype)
+
+
 class MXLinearSaved:
     """What the backward pass of a 4-bit layer needs: its input and weights along their columns
     (17/32 of a byte an element), and for experts the offsets."""
