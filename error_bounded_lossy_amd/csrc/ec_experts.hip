@@ -50,6 +50,8 @@ __global__ __launch_bounds__(kSortThreads) void expert_count(const void* ids, ui
 // it (and of all, for the offsets), then ranks its choices 1024 at a time: a
 // rank is the number of equal choices before it in its wave, in the waves
 // before it and in the rounds before.  A single part counts for itself.
+// Bound by its chain of loads, barriers and LDS sums: 6.3 us for 65536 choices
+// in 64 parts (after 4.6 us of counting), 3.6 us for 256 in one.
 __global__ __launch_bounds__(kSortThreads) void expert_place(
     const void* ids, uint32_t wide, uint64_t n, uint32_t experts, uint32_t per, uint32_t parts,
     const uint32_t* counts, int32_t* order, int32_t* place, int32_t* offsets) {
@@ -64,21 +66,16 @@ __global__ __launch_bounds__(kSortThreads) void expert_place(
   if (counts) {
     // 16 loads at a time: a latency each would be most of this kernel's time
     if (tid < cols) {
-      uint32_t p = 0;
-      for (; p + 16 <= parts; p += 16) {
+      for (uint32_t p = 0; p < parts; p += 16) {
         uint32_t c[16];
 #pragma unroll
-        for (int i = 0; i < 16; i++) c[i] = counts[(uint64_t)(p + i) * cols + tid];
+        for (int i = 0; i < 16; i++)
+          c[i] = p + i < parts ? counts[(uint64_t)(p + i) * cols + tid] : 0;
 #pragma unroll
         for (int i = 0; i < 16; i++) {
           before += p + i < blockIdx.x ? c[i] : 0;
           all += c[i];
         }
-      }
-      for (; p < parts; p++) {
-        const uint32_t c = counts[(uint64_t)p * cols + tid];
-        before += p < blockIdx.x ? c : 0;
-        all += c;
       }
     }
   } else {
@@ -202,6 +199,7 @@ __device__ __forceinline__ void clear_rows(T* xs, const Shape& s, const At& a, u
       store_eight(xs + r * s.cols + c * 8, (int64_t)s.cols - c * 8, Eight<T>{}, s.past);
 }
 
+// 16384 tokens, 4 choices, 4096 bf16: 109 us (6.2 TB/s).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void expert_dispatch(const T* __restrict__ x, Shape s,
                                                             const int32_t* __restrict__ place,
@@ -248,7 +246,9 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch_mx(
 
 // y[t] = sum over the choices of w (or 1) times the choice's row, in fp32 and
 // in the choices' order.  A lane has PIECES pieces of J rows in flight, and
-// places and weights are looked up once for all of them.
+// places and weights are looked up once for all of them.  16384 tokens, 4
+// choices, 4096 bf16: 139-145 us with weights, 124 without (4.7 and 5.4 TB/s);
+// with one piece 151 and 131.
 template <typename T, bool WEIGHTED, int PIECES>
 __global__ __launch_bounds__(kThreads) void expert_gather(const T* __restrict__ ys, Shape s,
                                                           const int32_t* __restrict__ place,
@@ -305,6 +305,7 @@ __global__ __launch_bounds__(kThreads) void expert_gather(const T* __restrict__ 
 // One pass over dy and ys: dys' rows and the products for dweights.  PIECES
 // of dy stay in registers while the choices' rows go by, so a row of dy is
 // read once where 2^shift lanes hold it (up to 8 PIECES 2^shift elements).
+// 16384 tokens, 4 choices, 4096 bf16: 210 us (5.8 TB/s).
 template <typename T, int PIECES>
 __global__ __launch_bounds__(kThreads) void expert_combine_back(
     const T* __restrict__ dy, const T* __restrict__ ys, Shape s, const int32_t* __restrict__ place,
@@ -408,10 +409,11 @@ bool fine(const void* p, size_t to) { return p && aligned(p, to); }
     default: { using T = bf16_t; call; } break;    \
   }
 
-// parts of the sort: one where a workgroup does it all in a few rounds, else
-// up to 256, so that adding up the parts before stays short
+// Parts of the sort: one where a workgroup does it all in two rounds (2048
+// choices: 5.9 us, in parts 6.1; 4096: 9.1 and 6.7), else up to 256, so that
+// adding up the parts before stays short.
 uint32_t sort_parts(uint64_t n) {
-  if (n <= 4 * kPart) return 1;
+  if (n <= 2 * kPart) return 1;
   const uint64_t p = ceil_div(n, kPart);
   return p > 256 ? 256 : (uint32_t)p;
 }

@@ -57,6 +57,10 @@ struct Product {
 // xor bits 1 and 2 of the row, so that 8 lanes of consecutive rows read 8
 // different 16-byte columns of 128.
 //
+// 8192 x 8192 x 8192 in bf16: 300 us (3.7 PFLOP/s), of which the instructions
+// alone take 270 at the clock that random codes leave (202 on zeros); loads and
+// LDS reads alone take 220.
+//
 // Scales come 16 bytes a row, once in four stages, through registers: 4 bytes
 // a row and stage would be as many requests of the caches as the codes are
 // (half of the L2 cache's requests, measured).
@@ -390,15 +394,17 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx_tiles(const Produ
 
 // ---------------------------------------------------------------- few rows
 
-// Up to 16 rows (of a group) at a time against 16 NT columns a workgroup: what
-// counts is reading b once, at full bandwidth.  The waves divide the
-// contraction in pieces of 512 elements; a lane loads 16 bytes of a row of b
-// and an instruction's 4 lanes of a row 64 bytes, straight into registers.
+// Up to 16 rows (of a group) against 16 NT columns a workgroup: what counts is
+// reading b once, at full bandwidth.  The waves divide the contraction in
+// pieces of 512 elements; a lane loads 16 bytes of a row of b and an
+// instruction's 4 lanes of a row 64 bytes, straight into registers.
 // With x unquantized (T), the workgroup quantizes its rows into LDS first,
 // while the first loads of b are in flight.
 //
 // A wave keeps two loads of 4 KiB and more in flight: the pieces of two rounds
 // (SETS = 2) where it has several, else those of two column tiles (NT = 2).
+// One row by 8192 x 8192: 8.7 us, 4.1 TB/s of the weights.  Rows of an expert
+// past 16 go to other workgroups, so that a crowded expert does not wait.
 constexpr uint32_t kFewCols = 16, kFewRows = 16, kFewWaves = 8;
 constexpr uint32_t kPiece = 512;
 
@@ -419,7 +425,7 @@ struct Few {
   const int32_t* offsets;
   uint64_t rows;
   uint32_t cols, depth, experts, n_tiles;
-  uint32_t held;  // rows that LDS holds (quantized here)
+  uint32_t held, shift;  // rows of a workgroup: up to held, of groups 2^shift = held
 };
 
 // A piece of b: 4 steps of 128 elements, and their scale bytes, whole words
@@ -437,26 +443,31 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void mx_few(const Few p) {
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t waves = blockDim.x >> 6;
   const uint32_t r = lane & 15, g = lane >> 4;
-  const uint32_t tn = blockIdx.x % p.n_tiles, e = blockIdx.x / p.n_tiles;
+  const uint32_t tn = blockIdx.x % p.n_tiles;
   const uint32_t n0 = tn * kFewCols * NT;
-  uint64_t first = 0, count = p.rows;
+  uint64_t row0 = 0;
+  uint32_t here = (uint32_t)p.rows;
   T* y = (T*)p.y;
   const uint8_t *bc = p.b.codes, *bs = p.b.scales;
   if (p.experts) {
-    if (e == p.experts) {  // rows of no group: zeros
-      int64_t f = p.offsets[p.experts];
-      f = f < 0 ? 0 : f;
+    const GroupTile gt =
+        find_tile(p.offsets, p.experts, p.rows, p.shift, blockIdx.x / p.n_tiles);
+    const uint64_t skip = (uint64_t)gt.local << p.shift;
+    if (gt.group == p.experts) {  // rows of no group: zeros
+      const int64_t f = p.offsets[p.experts];
+      const uint64_t m0 = (f < 0 ? 0 : f) + skip, end = min(m0 + p.held, p.rows);
       const uint32_t col = n0 + threadIdx.x % (kFewCols * NT);
       if (col < p.cols)
-        for (uint64_t m = (uint64_t)f + threadIdx.x / (kFewCols * NT); m < p.rows;
+        for (uint64_t m = m0 + threadIdx.x / (kFewCols * NT); m < end;
              m += blockDim.x / (kFewCols * NT))
           y[m * p.cols + col] = (T)0.0f;
       return;
     }
-    group_rows(p.offsets, e, p.rows, first, count);
-    if (count == 0) return;
-    bc += (uint64_t)e * p.cols * (p.depth / 2);
-    bs += (uint64_t)e * p.cols * (p.depth / 32);
+    if (skip >= gt.count) return;  // only with offsets out of order
+    row0 = gt.first + skip;
+    here = (uint32_t)min((uint64_t)p.held, gt.count - skip);
+    bc += (uint64_t)gt.group * p.cols * (p.depth / 2);
+    bs += (uint64_t)gt.group * p.cols * (p.depth / 32);
   }
   const uint32_t pitch = p.depth / 2, spitch = p.depth / 32;
   const uint32_t steps = p.depth / 128, pieces = (steps + 3) / 4;
@@ -468,7 +479,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void mx_few(const Few p) {
     gsb[t] = bs + (uint64_t)n * spitch;
   }
   const uint32_t lpitch = pitch + 16;  // rows of LDS start 4 banks apart
-  uint8_t* lscales = lds + p.held * lpitch;
+  uint8_t* lscales = lds + (uint32_t)min((uint64_t)p.held, p.rows) * lpitch;
 
   auto load = [&](Piece<NT>& f, uint32_t at) {
 #pragma unroll
@@ -486,78 +497,71 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void mx_few(const Few p) {
     }
   };
 
-  for (uint64_t m0 = 0; m0 < count; m0 += QUANTIZE ? p.held : kFewRows) {
-    const uint32_t here = (uint32_t)min((uint64_t)(QUANTIZE ? p.held : kFewRows), count - m0);
-    Piece<NT> f[SETS];
+  Piece<NT> f[SETS];
 #pragma unroll
-    for (int i = 0; i < SETS; i++)
-      if (wave + i * waves < pieces) load(f[i], wave + i * waves);
-    const uint64_t row0 = first + m0;
-    const uint32_t lr = min(r, here - 1);
-    const uint8_t *ga, *gsa;
-    if constexpr (QUANTIZE) {
-      const uint32_t chunks = p.depth / 8, total = here * chunks;
-      __syncthreads();  // the rows before are done
-      constexpr int Q = 2;  // loads in flight; four cost spilled registers
-      for (uint32_t i0 = threadIdx.x; i0 < total; i0 += Q * blockDim.x) {
-        Eight<T> v[Q];
-        uint32_t row[Q], c[Q];
+  for (int i = 0; i < SETS; i++)
+    if (wave + i * waves < pieces) load(f[i], wave + i * waves);
+  const uint32_t lr = min(r, here - 1);
+  const uint8_t *ga, *gsa;
+  if constexpr (QUANTIZE) {
+    const uint32_t chunks = p.depth / 8, total = here * chunks;
+    constexpr int Q = 4;  // loads in flight
+    for (uint32_t i0 = threadIdx.x; i0 < total; i0 += Q * blockDim.x) {
+      Eight<T> v[Q];
+      uint32_t row[Q], c[Q];
 #pragma unroll
-        for (int q = 0; q < Q; q++) {  // quads of lanes share a block
-          const uint32_t i = i0 + q * blockDim.x;
-          row[q] = i / chunks, c[q] = i - row[q] * chunks;
-          v[q] = load_eight((const T*)p.x + (row0 + row[q]) * p.stride + c[q] * 8,
-                            i < total ? (int64_t)p.raw_depth - c[q] * 8 : 0);
-        }
-#pragma unroll
-        for (int q = 0; q < Q; q++) {
-          if (i0 + q * blockDim.x >= total) break;
-          const Scale s = scale_of(exponent_of<T>(max_of_4_lanes(magnitude_of_eight(v[q]))));
-          *reinterpret_cast<uint32_t*>(lds + row[q] * lpitch + c[q] * 4) =
-              code_eight(v[q], s.size);
-          if ((c[q] & 3) == 0) lscales[row[q] * spitch + c[q] / 4] = (uint8_t)s.byte;
-        }
+      for (int q = 0; q < Q; q++) {  // quads of lanes share a block
+        const uint32_t i = i0 + q * blockDim.x;
+        row[q] = i / chunks, c[q] = i - row[q] * chunks;
+        v[q] = load_eight((const T*)p.x + (row0 + row[q]) * p.stride + c[q] * 8,
+                          i < total ? (int64_t)p.raw_depth - c[q] * 8 : 0);
       }
-      __syncthreads();
-      ga = lds + lr * lpitch + g * 16;
-      gsa = lscales + lr * spitch + g;
-    } else {
-      ga = p.a.codes + (row0 + lr) * pitch + g * 16;
-      gsa = p.a.scales + (row0 + lr) * spitch + g;
-    }
-    f32x4 acc[NT] = {};
-    for (uint32_t piece = wave; piece < pieces; piece += SETS * waves) {
 #pragma unroll
-      for (int i = 0; i < SETS; i++) {
-        const uint32_t now = piece + i * waves;
-        if (now >= pieces) break;
-#pragma unroll
-        for (int s = 0; s < 4; s++) {
-          const uint32_t step = now * 4 + s;
-          if (step < steps) {
-            const i32x4 fa = *reinterpret_cast<const i32x4*>(ga + step * 64);
-            const int sa = gsa[step * 4];
-#pragma unroll
-            for (int t = 0; t < NT; t++)
-              acc[t] = multiply16(f[i].b[t][s], fa, acc[t], (int)(f[i].s[t][s] >> (8 * g)), sa);
-          }
-        }
-        if (now + SETS * waves < pieces) load(f[i], now + SETS * waves);
+      for (int q = 0; q < Q; q++) {
+        if (i0 + q * blockDim.x >= total) break;
+        const Scale s = scale_of(exponent_of<T>(max_of_4_lanes(magnitude_of_eight(v[q]))));
+        *reinterpret_cast<uint32_t*>(lds + row[q] * lpitch + c[q] * 4) = code_eight(v[q], s.size);
+        if ((c[q] & 3) == 0) lscales[row[q] * spitch + c[q] / 4] = (uint8_t)s.byte;
       }
     }
-    // a lane has row r of y and columns 4 g .. 4 g + 3 of a tile; the waves'
-    // parts are added in their order
-#pragma unroll
-    for (int t = 0; t < NT; t++)
-      *reinterpret_cast<f32x4*>(&part[wave][(r * NT + t) * 16 + g * 4]) = acc[t];
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < here * 16 * NT; i += blockDim.x) {
-      float sum = 0;
-      for (uint32_t w = 0; w < waves; w++) sum += part[w][i];
-      const uint32_t col = n0 + i % (16 * NT);
-      if (col < p.cols) y[(row0 + i / (16 * NT)) * p.cols + col] = (T)sum;
+    ga = lds + lr * lpitch + g * 16;
+    gsa = lscales + lr * spitch + g;
+  } else {
+    ga = p.a.codes + (row0 + lr) * pitch + g * 16;
+    gsa = p.a.scales + (row0 + lr) * spitch + g;
+  }
+  f32x4 acc[NT] = {};
+  for (uint32_t piece = wave; piece < pieces; piece += SETS * waves) {
+#pragma unroll
+    for (int i = 0; i < SETS; i++) {
+      const uint32_t now = piece + i * waves;
+      if (now >= pieces) break;
+#pragma unroll
+      for (int s = 0; s < 4; s++) {
+        const uint32_t step = now * 4 + s;
+        if (step < steps) {
+          const i32x4 fa = *reinterpret_cast<const i32x4*>(ga + step * 64);
+          const int sa = gsa[step * 4];
+#pragma unroll
+          for (int t = 0; t < NT; t++)
+            acc[t] = multiply16(f[i].b[t][s], fa, acc[t], (int)(f[i].s[t][s] >> (8 * g)), sa);
+        }
+      }
+      if (now + SETS * waves < pieces) load(f[i], now + SETS * waves);
     }
-    if (m0 + (QUANTIZE ? p.held : kFewRows) < count) __syncthreads();
+  }
+  // a lane has row r of y and columns 4 g .. 4 g + 3 of a tile; the waves'
+  // parts are added in their order
+#pragma unroll
+  for (int t = 0; t < NT; t++)
+    *reinterpret_cast<f32x4*>(&part[wave][(r * NT + t) * 16 + g * 4]) = acc[t];
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < here * 16 * NT; i += blockDim.x) {
+    float sum = 0;
+    for (uint32_t w = 0; w < waves; w++) sum += part[w][i];
+    const uint32_t col = n0 + i % (16 * NT);
+    if (col < p.cols) y[(row0 + i / (16 * NT)) * p.cols + col] = (T)sum;
   }
 }
 
@@ -584,7 +588,9 @@ ec_status tiles_as(Product p, hipStream_t s) {
 // round of its workgroups (one a unit, 256 in all) may be nearly empty; of the
 // tiles of 128, two workgroups share a unit, and they cost 8% more for every
 // 1024 of the contraction (8192 x 8192 outputs: 78 against 73 us at 1024, 350
-// against 300 at 8192).  Rounds in units of the larger tile's, times 1024:
+// against 300 at 8192).  Costs in rounds of the larger tile, times 1024.
+// Tiles of 64 where fewer than 128 of 128 would run: 1024 x 4096 x 4096 takes
+// 22 us with tiles of 128 and 30 with 64, 64 x 4096 x 4096 10.4 with 64.
 template <typename T, int MODE>
 ec_status tiles_of(const Product& p, hipStream_t s) {
   const uint64_t groups = MODE == kTokens ? p.experts : 1;
@@ -612,9 +618,15 @@ ec_status tiles(const Product& p, int type, hipStream_t s) {
 template <typename T, int NT, int SETS>
 ec_status few_as(Few p, bool quantize, uint32_t waves, hipStream_t s) {
   p.n_tiles = (uint32_t)ceil_div(p.cols, kFewCols * NT);
-  const uint64_t blocks = (uint64_t)p.n_tiles * (p.experts ? p.experts + 1 : 1);
+  if (!quantize) p.held = kFewRows;
+  p.shift = __builtin_ctz(p.held);
+  // groups round up each, and the rows of no group once more
+  const uint64_t m =
+      p.experts ? ceil_div(p.rows, p.held) + (p.experts < p.rows ? p.experts : p.rows) + 1 : 1;
+  const uint64_t blocks = p.n_tiles * m;
   if (blocks > 0x7fffffffull) return EC_ERR_UNSUPPORTED;
-  const uint32_t lds = quantize ? p.held * (p.depth / 2 + 16 + p.depth / 32) : 0;
+  const uint32_t rows = p.rows < p.held ? (uint32_t)p.rows : p.held;  // what LDS has to hold
+  const uint32_t lds = quantize ? rows * (p.depth / 2 + 16 + p.depth / 32) : 0;
   if (quantize)
     hipLaunchKernelGGL((mx_few<T, true, NT, SETS>), dim3((uint32_t)blocks), dim3(64 * waves), lds,
                        s, p);
@@ -629,7 +641,8 @@ ec_status few_of(const Few& p, bool quantize, hipStream_t s) {
   const uint32_t pieces = (p.depth + kPiece - 1) / kPiece;
   const uint32_t waves = pieces < kFewWaves ? pieces : kFewWaves;
   const uint64_t columns = (uint64_t)p.cols * (p.experts ? p.experts : 1);
-  // two column tiles where a wave has one piece and 512 workgroups remain
+  // two column tiles where a wave has one piece and 512 workgroups remain: 4
+  // rows for each of 32 experts of 1024 x 2048 take 11.0 us, with one 12.4
   if (pieces <= kFewWaves && columns >= 512 * 2 * kFewCols)
     return few_as<T, 2, 1>(p, quantize, waves, s);
   return few_as<T, 1, 2>(p, quantize, waves, s);
@@ -663,22 +676,26 @@ ec_status check_groups(const int32_t* offsets, uint32_t groups) {
   return groups > EC_MX_MAX_GROUPS ? EC_ERR_UNSUPPORTED : EC_OK;
 }
 
-// How ec_mx_linear goes: rows (on average of a group) up to kFewRows take the
-// kernel for few rows.
+// How ec_mx_linear goes.  Measured with the quantization, us a call on the
+// GPU, for 1, 4, 8, 16 rows: 8192 x 8192 dense, quantizing in the product 8.7,
+// 10.9, 15.3, 16.7, before it 10.8, 12.2, 13.6, 16.2, tiles 16.4 each; 32
+// experts of 1024 x 2048 (rows of each) 10.8, 11.0, 13.1, 23, before it 12.5,
+// 12.9, 13.6, 15.8, tiles 12.0, 11.9, 12.0, 12.3.
 enum Way { kFewQuantizing, kFewStored, kTiled };
 constexpr uint32_t kFewLds = 48 * 1024;
 
-uint32_t held_rows(uint64_t rows, uint64_t padded) {
+// Rows that fit, a power of two (0: none).
+uint32_t held_rows(uint64_t padded) {
   const uint64_t each = padded / 2 + 16 + padded / 32;
-  uint64_t n = kFewLds / each;
-  if (n > kFewRows) n = kFewRows;
-  return (uint32_t)(n < rows ? n : rows);
+  uint32_t n = kFewRows;
+  while (n && n * each > kFewLds) n /= 2;
+  return n;
 }
 
 Way way_of(uint64_t rows, uint64_t padded, uint32_t experts) {
   const uint64_t mean = experts ? ceil_div(rows, experts) : rows;
-  if (mean > kFewRows) return kTiled;
-  return mean <= 8 && held_rows(rows, padded) >= mean ? kFewQuantizing : kFewStored;
+  if (mean <= 4 && held_rows(padded) >= mean) return kFewQuantizing;
+  return !experts && rows <= kFewRows ? kFewStored : kTiled;
 }
 
 }  // namespace
@@ -714,14 +731,6 @@ ec_status ec_mx_product_experts(const void* a_codes, const void* a_scales, uint6
   st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, y, type);
   if (st != EC_OK || rows == 0) return st;
   if (depth == 0) return EC_ERR_INVALID;
-  if (ceil_div(rows, experts) <= kFewRows) {
-    Few f{};
-    f.a = {(const uint8_t*)a_codes, (const uint8_t*)a_scales};
-    f.b = {(const uint8_t*)b_codes, (const uint8_t*)b_scales};
-    f.y = y, f.rows = rows, f.cols = (uint32_t)cols, f.depth = (uint32_t)depth;
-    f.offsets = offsets, f.experts = experts;
-    return few(f, type, false, (hipStream_t)stream);
-  }
   Product p{};
   p.a = {(const uint8_t*)a_codes, (const uint8_t*)a_scales};
   p.b = {(const uint8_t*)b_codes, (const uint8_t*)b_scales};
@@ -780,7 +789,7 @@ ec_status ec_mx_linear(const void* x, int type, uint64_t rows, uint64_t depth, u
     f.b = {(const uint8_t*)w_codes, (const uint8_t*)w_scales};
     f.y = y, f.rows = rows, f.cols = (uint32_t)cols, f.depth = (uint32_t)padded;
     f.offsets = offsets, f.experts = experts;
-    f.held = held_rows(rows, padded);
+    f.held = held_rows(padded);
     return few(f, type, true, (hipStream_t)stream);
   }
   uint8_t* codes = (uint8_t*)workspace;

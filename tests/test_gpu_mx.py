@@ -311,6 +311,25 @@ def test_experts_large_tiles(dtype):
     assert not y[sum(counts):].any() and not dx[sum(counts):].any() and not dw[1].any()
 
 
+@pytest.mark.parametrize("counts", [[0, 90, 0, 1, 17, 0, 0, 4] + [0] * 12, [500] + [0] * 63, [0] * 1023 + [40]],
+                         ids=lambda c: f"{len(c)}x{sum(c)}")
+@pytest.mark.parametrize("depth", [200, 9000])
+def test_experts_few_rows_on_average(counts, depth):
+    # few rows an expert on average, many for some: several workgroups share its columns
+    x, offsets = grouped(counts, 5, 1, depth, torch.bfloat16)
+    cols = 40 if len(counts) < 100 else 3
+    w = activations(2, len(counts), cols, depth, spread=1.0)
+    q = ec.mx_quantize(w)
+    stored = ec.mx_experts_product(ec.mx_quantize(x), q, offsets)
+    y = ec.mx_experts_linear(x, q, offsets)
+    for e, (a, b) in enumerate(parts(offsets)):
+        if a < b:
+            want = R.mm_bound(R.near(x[a:b]), R.near(w[e]), torch.bfloat16)
+            R.check(y[a:b], *want, f"y {e}")
+            R.check(stored[a:b], *want, f"stored {e}")
+    assert not y[sum(counts):].any() and not stored[sum(counts):].any()
+
+
 def test_experts_tiles_of_256():
     # enough rows and columns for the largest tile, in one round of workgroups
     counts = [2000, 1, 0, 1700, 300]
