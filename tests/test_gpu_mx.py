@@ -195,6 +195,16 @@ def test_linear_tiles(rows, depth, cols, dtype):
     R.check(ec.mx_linear(x, ec.mx_quantize(w)), y, bound)
 
 
+# rows past whole tiles that would start another round of them: few, and some
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,depth,cols", [(4100, 200, 4096), (2125, 300, 8190), (4111, 128, 4001)])
+def test_linear_rows_past_whole_tiles(rows, depth, cols, dtype):
+    x = activations(rows, rows, depth, dtype=dtype, spread=1.0)
+    w = activations(cols, cols, depth, dtype=dtype, spread=1.0)
+    y, bound = R.mm_bound(R.near(x), R.near(w), dtype)
+    R.check(ec.mx_linear(x, ec.mx_quantize(w)), y, bound)
+
+
 def test_scales_at_their_ends():
     # blocks near 2^-127 against blocks near 2^120, and results that are subnormal
     x = torch.randn(20, 256, generator=gen(1), device="cuda")
