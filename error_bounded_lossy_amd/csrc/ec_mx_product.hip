@@ -585,30 +585,38 @@ ec_status tiles_as(Product p, hipStream_t s) {
 }
 
 // The larger tile reads less and keeps the matrix units busier, but the last
-// round of its workgroups (one a unit, 256 in all) may be nearly empty; of the
-// tiles of 128, two workgroups share a unit, and they cost 8% more for every
-// 1024 of the contraction (8192 x 8192 outputs: 78 against 73 us at 1024, 350
-// against 300 at 8192).  Costs in rounds of the larger tile, times 1024.
+// round of its workgroups (one a unit, 256 in all) may be nearly empty, and
+// nothing hides where it starts and ends; of the tiles of 128, two workgroups
+// share a unit.  Measured for 8192 x 8192 outputs in bf16, a contraction of
+// 128, 512, 1024, 2048, 4096, 8192, us: large 37, 49, 64, 101, 166, 288, small
+// 31, 47, 76, 122, 216, 388: about 8 and 8 more for each 1024 a round of 256,
+// and 3.5 and 5.5 more a round of 512.  Finding a group's rows adds 5 to a
+// round of large ones and tokens' parts 3 (16 groups, 16384 x 2048 x 2048:
+// large 62 and 85 us, small 59 and 79; tokens of 4 groups, 4096 x 4096 x 4096:
+// large 71, small 77).  Costs in us times 1024.
+//
 // Tiles of 64 where fewer than 128 of 128 would run: 1024 x 4096 x 4096 takes
 // 22 us with tiles of 128 and 30 with 64, 64 x 4096 x 4096 10.4 with 64.
 struct Tiles {
   uint64_t large, small;            // how many
   uint64_t cost_large, cost_small;  // too few large ones: more than anything
 };
-Tiles tiles_for(uint64_t rows, uint64_t cols, uint64_t depth, uint64_t groups, uint64_t extra) {
+Tiles tiles_for(int mode, uint64_t rows, uint64_t cols, uint64_t depth, uint64_t groups) {
+  const uint64_t extra = mode == kExperts ? groups / 2 : 0;  // half a tile more for each
+  const uint64_t sets = mode == kTokens ? groups : 1;
   Tiles t;
-  t.large = (ceil_div(rows, 256) + extra) * ceil_div(cols, 256) * groups;
-  t.small = (ceil_div(rows, 128) + extra) * ceil_div(cols, 128) * groups;
-  t.cost_large = t.large < 192 ? ~0ull >> 1 : ceil_div(t.large, 256) * 1024;
-  t.cost_small = ceil_div(t.small, 512) * (512 + depth / 25);
+  t.large = (ceil_div(rows, 256) + extra) * ceil_div(cols, 256) * sets;
+  t.small = (ceil_div(rows, 128) + extra) * ceil_div(cols, 128) * sets;
+  const uint64_t start = mode == kDense ? 8 : mode == kExperts ? 13 : 11;
+  t.cost_large = t.large < 192 ? ~0ull >> 1 : ceil_div(t.large, 256) * (start * 1024 + depth * 8);
+  t.cost_small = ceil_div(t.small, 512) * (3584 + depth * 11 / 2);
   return t;
 }
 
 template <typename T, int MODE>
 ec_status tiles_of(const Product& p, hipStream_t s) {
-  // rows of experts: half a tile more for each
-  const Tiles t = tiles_for(p.rows, p.cols, MODE == kTokens ? p.tokens / p.experts : p.depth,
-                            MODE == kTokens ? p.experts : 1, MODE == kExperts ? p.experts / 2 : 0);
+  const Tiles t = tiles_for(MODE, p.rows, p.cols,
+                            MODE == kTokens ? p.tokens / p.experts : p.depth, p.experts);
   if (t.cost_large <= t.cost_small) return tiles_as<4, 4, T, MODE>(p, s);
   if (t.small >= 128) return tiles_as<2, 2, T, MODE>(p, s);
   return tiles_as<1, 1, T, MODE>(p, s);
@@ -616,13 +624,15 @@ ec_status tiles_of(const Product& p, hipStream_t s) {
 
 // Rows (a multiple of 256) whose large tiles go first where the rest, which
 // would begin another round, goes to a launch of its own: under 256 rows take
-// about a quarter of a round (4096 x 4096: 8 to 10 us against 43).  Else 0.
+// 8 to 10 us by 4096 x 4096, a round of large tiles 43 (4100 rows: 50, with
+// tiles of 128 65, large ones 72).  Else 0.
 uint64_t rows_first(uint64_t rows, uint64_t cols, uint64_t depth) {
   const uint64_t main = rows / 256 * 256;
   if (main == 0 || main == rows) return 0;
-  const Tiles all = tiles_for(rows, cols, depth, 1, 0), t = tiles_for(main, cols, depth, 1, 0);
+  const Tiles all = tiles_for(kDense, rows, cols, depth, 1);
+  const Tiles t = tiles_for(kDense, main, cols, depth, 1);
   const uint64_t best = all.cost_large < all.cost_small ? all.cost_large : all.cost_small;
-  return t.cost_large + 256 < best ? main : 0;
+  return t.cost_large + 4 * 1024 + depth * 3 / 2 < best ? main : 0;
 }
 
 template <int MODE>

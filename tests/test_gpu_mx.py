@@ -205,6 +205,14 @@ def test_linear_rows_past_whole_tiles(rows, depth, cols, dtype):
     R.check(ec.mx_linear(x, ec.mx_quantize(w)), y, bound)
 
 
+@pytest.mark.parametrize("rows,depth,cols", [(4111, 2100, 4096), (4226, 2000, 4090), (8200, 1500, 2040)])
+def test_linear_rows_past_whole_tiles_of_long_contractions(rows, depth, cols):
+    x = activations(rows, rows, depth, spread=1.0)
+    w = activations(cols, cols, depth, spread=1.0)
+    y, bound = R.mm_bound(R.near(x), R.near(w), torch.bfloat16)
+    R.check(ec.mx_linear(x, ec.mx_quantize(w)), y, bound)
+
+
 def test_scales_at_their_ends():
     # blocks near 2^-127 against blocks near 2^120, and results that are subnormal
     x = torch.randn(20, 256, generator=gen(1), device="cuda")
@@ -350,6 +358,19 @@ def test_experts_tiles_of_256():
         if a < b:
             R.check(y[a:b], *R.mm_bound(R.near(x[a:b]), R.near(w[e]), torch.bfloat16), f"y {e}")
     assert not y[sum(counts):].any()
+
+
+def test_experts_training_with_tiles_of_256():
+    # contractions long enough for the largest tile in all three products
+    x, offsets = grouped([2400, 2500], 0, 1, 2600, torch.bfloat16)
+    w = activations(2, 2, 2500, 2600, spread=1.0)
+    dy = activations(3, 4900, 2500, spread=1.0)
+    y, saved = ec.mx_experts_forward(x, w, offsets)
+    dx, dw = ec.mx_experts_backward(dy, saved)
+    for e, (a, b) in enumerate(parts(offsets)):
+        R.check(y[a:b], *R.mm_bound(R.near(x[a:b]), R.near(w[e]), torch.bfloat16), f"y {e}")
+        R.check(dx[a:b], *R.mm_bound(R.near(dy[a:b]), R.near(w[e].t()), torch.bfloat16), f"dx {e}")
+        R.check(dw[e], *R.mm_bound(R.near(dy[a:b].t()), R.near(x[a:b].t()), torch.bfloat16), f"dw {e}")
 
 
 @pytest.mark.parametrize("offsets", [[0, 50, 20, 90], [-5, 10, 400, 90], [70, 70, 10, 0], [0, 0, 0, 500]],
