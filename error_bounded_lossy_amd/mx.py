@@ -9,6 +9,8 @@ caller orders that stream after what produced the inputs).
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _binding as _b
@@ -48,7 +50,9 @@ class MXTensor:
     """A tensor in the 4-bit form along its last dimension, of `cols` elements:
     codes, uint8 [..., padded / 2], and scales, uint8 [..., padded / 32]."""
 
-    __slots__ = ("codes", "scales", "cols")
+    # What the library makes holds both in one allocation, `home`, codes first, and has them as
+    # tensors only when asked: an allocation or a view costs the host as much as a small kernel.
+    __slots__ = ("cols", "padded", "lead", "home", "codes_ptr", "scales_ptr", "_codes", "_scales")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
         p = (cols + 127) // 128 * 128
@@ -59,30 +63,45 @@ class MXTensor:
                 or codes.device != scales.device):
             _refuse("MXTensor: uint8 codes [..., padded / 2] and scales [..., padded / 32], "
                     "contiguous and on one device, are wanted")
-        self.codes, self.scales, self.cols = codes, scales, cols
+        self.cols, self.padded, self.lead, self.home = cols, p, codes.shape[:-1], codes
+        self._codes, self._scales = codes, scales
+        self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            n = self.home.numel() // 17 * 16
+            self._codes = self.home[:n].view(*self.lead, self.padded // 2)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            n = self.home.numel() // 17 * 16
+            self._scales = self.home[n:].view(*self.lead, self.padded // 32)
+        return self._scales
 
     @property
     def shape(self) -> torch.Size:
-        return self.codes.shape[:-1] + (self.cols,)
+        return torch.Size((*self.lead, self.cols))
 
     @property
     def device(self) -> torch.device:
-        return self.codes.device
+        return self.home.device
 
     def numel_bytes(self) -> int:
-        return self.codes.numel() + self.scales.numel()
-
-
-def _made(codes, scales, cols) -> MXTensor:
-    m = object.__new__(MXTensor)
-    m.codes, m.scales, m.cols = codes, scales, cols
-    return m
+        return math.prod(self.lead) * (self.padded // 32) * 17
 
 
 def _empty(lead, cols, like, p=None) -> MXTensor:
-    p = (cols + 127) // 128 * 128 if p is None else p
-    codes = like.new_empty((*lead, p // 2), dtype=torch.uint8)
-    return _made(codes, codes.new_empty((*lead, p // 32)), cols)
+    m = object.__new__(MXTensor)
+    m.cols, m.padded, m.lead = cols, (cols + 127) // 128 * 128 if p is None else p, lead
+    n = math.prod(lead) * (m.padded // 2)  # a multiple of 64: the scales are aligned behind
+    m.home = like.new_empty(n // 16 * 17, dtype=torch.uint8)
+    m.codes_ptr = m.home.data_ptr()
+    m.scales_ptr = m.codes_ptr + n
+    m._codes = m._scales = None
+    return m
 
 
 def mx_quantize(x: torch.Tensor, stream=None) -> MXTensor:
@@ -95,7 +114,7 @@ def mx_quantize(x: torch.Tensor, stream=None) -> MXTensor:
     r, stride = _rows(x)
     q = _empty(x.shape[:-1], x.shape[-1], x)
     _b.check(_b.lib().ec_mx_quantize(r.data_ptr(), kind, r.shape[0], r.shape[1], stride,
-                                     q.codes.data_ptr(), q.scales.data_ptr(),
+                                     q.codes_ptr, q.scales_ptr,
                                      _b.current_stream(x)), "ec_mx_quantize")
     return q
 
@@ -120,22 +139,22 @@ def mx_quantize_both(x: torch.Tensor, stream=None) -> tuple[MXTensor, MXTensor]:
     if rows and batch:
         _b.check(_b.lib().ec_mx_quantize_both(
             x.data_ptr(), kind, batch, rows, cols, batch_stride, stride,
-            a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
+            a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr,
             _b.current_stream(x)), "ec_mx_quantize_both")
     return a, b
 
 
 def mx_dequantize(q: MXTensor, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """The values that q holds, rounded once to dtype."""
-    if stream is not None or _b.elsewhere(q.codes):
+    if stream is not None or _b.elsewhere(q.home):
         return _b.on_stream(mx_dequantize, (q, dtype), stream)
     kind = TYPES.get(dtype)
-    if kind is None or not q.codes.is_cuda or q.cols == 0:
+    if kind is None or not q.home.is_cuda or q.cols == 0:
         _refuse("mx_dequantize: a nonempty row on the GPU and float32, float16 or bfloat16 are wanted")
-    lead = q.codes.shape[:-1]
-    y = q.codes.new_empty((*lead, q.cols), dtype=dtype)
+    lead = q.lead
+    y = q.home.new_empty((*lead, q.cols), dtype=dtype)
     rows = y.numel() // q.cols
-    _b.check(_b.lib().ec_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), rows, q.cols,
+    _b.check(_b.lib().ec_mx_dequantize(q.codes_ptr, q.scales_ptr, rows, q.cols,
                                        y.data_ptr(), kind, q.cols, _b.current_stream(y)),
              "ec_mx_dequantize")
     return y
@@ -151,34 +170,34 @@ def _offsets(offsets: torch.Tensor, groups: int, device, what: str) -> torch.Ten
 def mx_product(a: MXTensor, b: MXTensor, dtype: torch.dtype = torch.bfloat16,
                stream=None) -> torch.Tensor:
     """a b^T [rows, cols] of a [rows, depth] and b [cols, depth], summed in fp32, rounded once."""
-    if stream is not None or _b.elsewhere(a.codes):
+    if stream is not None or _b.elsewhere(a.home):
         return _b.on_stream(mx_product, (a, b, dtype), stream)
     kind = TYPES.get(dtype)
-    if (kind is None or a.codes.dim() != 2 or b.codes.dim() != 2 or a.cols != b.cols or a.cols == 0
-            or not a.codes.is_cuda or a.codes.device != b.codes.device):
+    if (kind is None or len(a.lead) != 1 or len(b.lead) != 1 or a.cols != b.cols or a.cols == 0
+            or not a.home.is_cuda or a.home.device != b.home.device):
         _refuse("mx_product: [rows, depth] and [cols, depth] on one GPU are wanted")
-    rows, cols = a.codes.shape[0], b.codes.shape[0]
-    y = torch.empty((rows, cols), dtype=dtype, device=a.codes.device)
-    _b.check(_b.lib().ec_mx_product(a.codes.data_ptr(), a.scales.data_ptr(), rows,
-                                    b.codes.data_ptr(), b.scales.data_ptr(), cols,
-                                    a.codes.shape[1] * 2, y.data_ptr(), kind,
+    rows, cols = a.lead[0], b.lead[0]
+    y = a.home.new_empty((rows, cols), dtype=dtype)
+    _b.check(_b.lib().ec_mx_product(a.codes_ptr, a.scales_ptr, rows,
+                                    b.codes_ptr, b.scales_ptr, cols,
+                                    a.padded, y.data_ptr(), kind,
                                     _b.current_stream(y)), "ec_mx_product")
     return y
 
 
 def _linear(x, w, offsets, experts, what):
     kind = _type(x, what)
-    cols, depth = w.codes.shape[-2], x.shape[-1]
-    if w.cols != depth or depth == 0 or w.codes.device != x.device:
+    cols, depth = w.lead[-1], x.shape[-1]
+    if w.cols != depth or depth == 0 or w.home.device != x.device:
         _refuse(f"{what}: weights [.., cols, depth] on the device of x [.., depth] are wanted")
     r, stride = _rows(x)
     rows = r.shape[0]
     L = _b.lib()
     y = x.new_empty((*x.shape[:-1], cols))
     need = L.ec_mx_linear_workspace_bytes(rows, depth, cols, experts)
-    ws = w.codes.new_empty(need).data_ptr() if need else None
-    _b.check(L.ec_mx_linear(r.data_ptr(), kind, rows, depth, stride, w.codes.data_ptr(),
-                            w.scales.data_ptr(), cols,
+    ws = w.home.new_empty(need).data_ptr() if need else None
+    _b.check(L.ec_mx_linear(r.data_ptr(), kind, rows, depth, stride, w.codes_ptr,
+                            w.scales_ptr, cols,
                             offsets.data_ptr() if experts else None, experts, y.data_ptr(), ws,
                             need, _b.current_stream(x)), "ec_mx_linear")
     return y
@@ -188,7 +207,7 @@ def mx_linear(x: torch.Tensor, w: MXTensor, stream=None) -> torch.Tensor:
     """x w^T with x [..., depth] quantized on the way and weights w [cols, depth]."""
     if stream is not None or _b.elsewhere(x):
         return _b.on_stream(mx_linear, (x, w), stream)
-    if w.codes.dim() != 2:
+    if len(w.lead) != 1:
         _refuse("mx_linear: weights [cols, depth] are wanted")
     return _linear(x, w, None, 0, "mx_linear")
 
@@ -199,9 +218,9 @@ def mx_experts_linear(x: torch.Tensor, w: MXTensor, offsets: torch.Tensor,
     of expert e, w [experts, cols, depth]; zeros in rows of no expert."""
     if stream is not None or _b.elsewhere(x):
         return _b.on_stream(mx_experts_linear, (x, w, offsets), stream)
-    if w.codes.dim() != 3 or x.dim() != 2:
+    if len(w.lead) != 2 or x.dim() != 2:
         _refuse("mx_experts_linear: x [rows, depth] and weights [experts, cols, depth] are wanted")
-    experts = w.codes.shape[0]
+    experts = w.lead[0]
     _offsets(offsets, experts, x.device, "mx_experts_linear")
     return _linear(x, w, offsets, experts, "mx_experts_linear")
 
@@ -210,13 +229,13 @@ def mx_experts_product(a: MXTensor, b: MXTensor, offsets: torch.Tensor,
                        dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """mx_experts_linear of rows that are in the 4-bit form already, as expert_dispatch_mx makes
     them: a [rows, depth], b [experts, cols, depth]."""
-    if stream is not None or _b.elsewhere(a.codes):
+    if stream is not None or _b.elsewhere(a.home):
         return _b.on_stream(mx_experts_product, (a, b, offsets, dtype), stream)
-    if (dtype not in TYPES or a.codes.dim() != 2 or b.codes.dim() != 3 or a.cols != b.cols
-            or a.cols == 0 or 0 in b.codes.shape or not a.codes.is_cuda
-            or a.codes.device != b.codes.device):
+    if (dtype not in TYPES or len(a.lead) != 1 or len(b.lead) != 2 or a.cols != b.cols
+            or a.cols == 0 or 0 in b.lead or not a.home.is_cuda
+            or a.home.device != b.home.device):
         _refuse("mx_experts_product: [rows, depth] and [experts, cols, depth] on one GPU are wanted")
-    _offsets(offsets, b.codes.shape[0], a.codes.device, "mx_experts_product")
+    _offsets(offsets, b.lead[0], a.home.device, "mx_experts_product")
     return _experts_product(a, b, offsets, dtype)
 
 
@@ -250,8 +269,8 @@ def mx_linear_backward(dy: torch.Tensor, saved: MXLinearSaved, stream=None):
             or dy.shape != (saved.rows, saved.w.cols) or dy.device != saved.x.device):
         _refuse("mx_linear_backward: dy [rows, cols] of the forward's type is wanted")
     if saved.rows == 0:
-        return (dy.new_zeros(0, saved.x.codes.shape[0]),
-                dy.new_zeros(dy.shape[1], saved.x.codes.shape[0]))
+        return (dy.new_zeros(0, saved.x.lead[0]),
+                dy.new_zeros(dy.shape[1], saved.x.lead[0]))
     dr, dc = mx_quantize_both(dy)
     return mx_product(dr, saved.w, dy.dtype), mx_product(dc, saved.x, dy.dtype)
 
@@ -264,20 +283,20 @@ def _quantize_groups(x, offsets, experts, rows_too=True):
     b = _empty((cols,), rows, x, int(L.ec_mx_padded_groups(rows, experts)))
     if rows:
         _b.check(L.ec_mx_quantize_groups(r.data_ptr(), TYPES[x.dtype], rows, cols, stride,
-                                         offsets.data_ptr(), experts, a.codes.data_ptr(),
-                                         a.scales.data_ptr(), b.codes.data_ptr(),
-                                         b.scales.data_ptr(), _b.current_stream(x)),
+                                         offsets.data_ptr(), experts, a.codes_ptr,
+                                         a.scales_ptr, b.codes_ptr,
+                                         b.scales_ptr, _b.current_stream(x)),
                  "ec_mx_quantize_groups")
     return a, b
 
 
 def _experts_product(a, b, offsets, dtype):
-    experts, cols = b.codes.shape[:2]
-    rows = a.codes.shape[0]
-    y = torch.empty((rows, cols), dtype=dtype, device=a.codes.device)
+    experts, cols = b.lead
+    rows = a.lead[0]
+    y = a.home.new_empty((rows, cols), dtype=dtype)
     _b.check(_b.lib().ec_mx_product_experts(
-        a.codes.data_ptr(), a.scales.data_ptr(), rows, b.codes.data_ptr(), b.scales.data_ptr(), cols,
-        a.codes.shape[1] * 2, offsets.data_ptr(), experts, y.data_ptr(), TYPES[dtype],
+        a.codes_ptr, a.scales_ptr, rows, b.codes_ptr, b.scales_ptr, cols,
+        a.padded, offsets.data_ptr(), experts, y.data_ptr(), TYPES[dtype],
         _b.current_stream(y)), "ec_mx_product_experts")
     return y
 
@@ -306,13 +325,13 @@ def mx_experts_backward(dy: torch.Tensor, saved: MXLinearSaved, stream=None):
     if (saved.offsets is None or dy.dim() != 2 or dy.dtype != saved.dtype
             or dy.shape != (saved.rows, saved.w.cols) or dy.device != saved.x.device):
         _refuse("mx_experts_backward: dy [rows, cols] of the forward's type is wanted")
-    experts, depth = saved.w.codes.shape[:2]
+    experts, depth = saved.w.lead
     cols = saved.w.cols
     dr, dc = _quantize_groups(dy, saved.offsets, experts)
     dx = _experts_product(dr, saved.w, saved.offsets, dy.dtype)
     dw = torch.empty((experts, cols, depth), dtype=dy.dtype, device=dy.device)
     _b.check(_b.lib().ec_mx_product_tokens(
-        dc.codes.data_ptr(), dc.scales.data_ptr(), cols, saved.x.codes.data_ptr(),
-        saved.x.scales.data_ptr(), depth, saved.rows, saved.offsets.data_ptr(), experts,
+        dc.codes_ptr, dc.scales_ptr, cols, saved.x.codes_ptr,
+        saved.x.scales_ptr, depth, saved.rows, saved.offsets.data_ptr(), experts,
         dw.data_ptr(), TYPES[dy.dtype], _b.current_stream(dy)), "ec_mx_product_tokens")
     return dx, dw
