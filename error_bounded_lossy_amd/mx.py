@@ -50,12 +50,14 @@ class MXTensor:
     """A tensor in the 4-bit form along its last dimension, of `cols` elements:
     codes, uint8 [..., padded / 2], and scales, uint8 [..., padded / 32]."""
 
-    # What the library makes holds both in one allocation, `home`, codes first, and has them as
-    # tensors only when asked: an allocation or a view costs the host as much as a small kernel.
-    __slots__ = ("cols", "padded", "lead", "home", "codes_ptr", "scales_ptr", "_codes", "_scales")
+    # What the library makes holds both in one allocation, `home`, codes first (`_scales` is None),
+    # and has them as tensors only when asked: an allocation or a view costs the host as much as a
+    # small kernel.  Addresses are taken from the tensors at each call: copies, and tensors whose
+    # memory the caller replaces, are read where they are.
+    __slots__ = ("cols", "padded", "lead", "home", "_scales", "_split")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
-        p = (cols + 127) // 128 * 128
+        p = padded(cols)
         if (codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or cols < 0
                 or codes.shape[-1] * 2 != p or scales.shape[-1] * 32 != p
                 or codes.shape[:-1] != scales.shape[:-1]
@@ -63,23 +65,48 @@ class MXTensor:
                 or codes.device != scales.device):
             _refuse("MXTensor: uint8 codes [..., padded / 2] and scales [..., padded / 32], "
                     "contiguous and on one device, are wanted")
-        self.cols, self.padded, self.lead, self.home = cols, p, codes.shape[:-1], codes
-        self._codes, self._scales = codes, scales
-        self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
+        self.cols, self.padded, self.lead = cols, p, codes.shape[:-1]
+        self.home, self._scales, self._split = codes, scales, codes.numel()
+
+    def __reduce__(self):
+        return _restored, (self.home, self._scales, tuple(self.lead), self.cols, self.padded)
+
+    def _whole(self) -> torch.Tensor:
+        """home, if it still has the size that codes and scales take."""
+        if self.home.numel() != self._split // 16 * 17:
+            _refuse("MXTensor: its memory was replaced by some of another size")
+        return self.home
+
+    def _given(self, t: torch.Tensor, per: int) -> torch.Tensor:
+        """t, if it still has the form that the constructor checked."""
+        if (t.dtype != torch.uint8 or not t.is_contiguous()
+                or t.shape != (*self.lead, self.padded // per) or t.device != self.home.device):
+            _refuse("MXTensor: its memory was replaced by some of another form")
+        return t
 
     @property
     def codes(self) -> torch.Tensor:
-        if self._codes is None:
-            n = self.home.numel() // 17 * 16
-            self._codes = self.home[:n].view(*self.lead, self.padded // 2)
-        return self._codes
+        if self._scales is not None:
+            return self.home
+        return self._whole()[:self._split].view(*self.lead, self.padded // 2)
 
     @property
     def scales(self) -> torch.Tensor:
+        if self._scales is not None:
+            return self._scales
+        return self._whole()[self._split:].view(*self.lead, self.padded // 32)
+
+    @property
+    def codes_ptr(self) -> int:
         if self._scales is None:
-            n = self.home.numel() // 17 * 16
-            self._scales = self.home[n:].view(*self.lead, self.padded // 32)
-        return self._scales
+            return self._whole().data_ptr()
+        return self._given(self.home, 2).data_ptr()
+
+    @property
+    def scales_ptr(self) -> int:
+        if self._scales is None:
+            return self._whole().data_ptr() + self._split
+        return self._given(self._scales, 32).data_ptr()
 
     @property
     def shape(self) -> torch.Size:
@@ -95,12 +122,26 @@ class MXTensor:
 
 def _empty(lead, cols, like, p=None) -> MXTensor:
     m = object.__new__(MXTensor)
-    m.cols, m.padded, m.lead = cols, (cols + 127) // 128 * 128 if p is None else p, lead
-    n = math.prod(lead) * (m.padded // 2)  # a multiple of 64: the scales are aligned behind
-    m.home = like.new_empty(n // 16 * 17, dtype=torch.uint8)
-    m.codes_ptr = m.home.data_ptr()
-    m.scales_ptr = m.codes_ptr + n
-    m._codes = m._scales = None
+    m.cols, m.padded, m.lead = cols, padded(cols) if p is None else p, lead
+    # bytes of codes, the scales behind: a multiple of 64, so both are aligned
+    m._split = math.prod(lead) * (m.padded // 2)
+    m.home = like.new_empty(m._split // 16 * 17, dtype=torch.uint8)
+    m._scales = None
+    return m
+
+
+def _restored(home, scales, lead, cols, p) -> MXTensor:
+    """An MXTensor of the parts that a copy or a file holds."""
+    m = object.__new__(MXTensor)
+    m.cols, m.padded, m.lead, m.home, m._scales = cols, p, torch.Size(lead), home, scales
+    m._split = math.prod(lead) * (p // 2)
+    if scales is not None:
+        m._given(home, 2)
+        m._given(scales, 32)
+    elif home.dtype != torch.uint8 or not home.is_contiguous() or m._whole() is not home:
+        _refuse("MXTensor: uint8 memory in one piece is wanted")
+    if cols < 0 or p % 128 or p < cols:
+        _refuse("MXTensor: a padded row is a multiple of 128 elements")
     return m
 
 
