@@ -96,7 +96,7 @@ def expert_dispatch_mx(x: torch.Tensor, routing: Routing, stream=None) -> MXTens
     q = _empty((r.tokens * r.choices,), cols, x)
     _b.check(_b.lib().ec_expert_dispatch_mx(x.data_ptr(), kind, r.tokens, cols,
                                             r.place.data_ptr(), r.choices, r.offsets.data_ptr(),
-                                            r.experts, q.codes_ptr, q.scales_ptr,
+                                            r.experts, *q.pointers(),
                                             _b.current_stream(x)), "ec_expert_dispatch_mx")
     return q
 

@@ -54,7 +54,7 @@ class MXTensor:
     # and has them as tensors only when asked: an allocation or a view costs the host as much as a
     # small kernel.  Addresses are taken from the tensors at each call: copies, and tensors whose
     # memory the caller replaces, are read where they are.
-    __slots__ = ("cols", "padded", "lead", "home", "_scales", "_split")
+    __slots__ = ("cols", "padded", "lead", "home", "_scales", "_split", "_forms")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
         p = padded(cols)
@@ -66,7 +66,8 @@ class MXTensor:
             _refuse("MXTensor: uint8 codes [..., padded / 2] and scales [..., padded / 32], "
                     "contiguous and on one device, are wanted")
         self.cols, self.padded, self.lead = cols, p, codes.shape[:-1]
-        self.home, self._scales, self._split = codes, scales, codes.numel()
+        self.home, self._scales = codes, scales
+        self._split, self._forms = None, (codes.shape, scales.shape)
 
     def __reduce__(self):
         return _restored, (self.home, self._scales, tuple(self.lead), self.cols, self.padded)
@@ -77,12 +78,12 @@ class MXTensor:
             _refuse("MXTensor: its memory was replaced by some of another size")
         return self.home
 
-    def _given(self, t: torch.Tensor, per: int) -> torch.Tensor:
-        """t, if it still has the form that the constructor checked."""
-        if (t.dtype != torch.uint8 or not t.is_contiguous()
-                or t.shape != (*self.lead, self.padded // per) or t.device != self.home.device):
+    def _given(self, t: torch.Tensor, form: torch.Size) -> int:
+        """Where t is, if it still has the form that the constructor checked."""
+        if (t.shape != form or t.dtype is not torch.uint8 or not t.is_contiguous()
+                or t.get_device() != self.home.get_device()):
             _refuse("MXTensor: its memory was replaced by some of another form")
-        return t
+        return t.data_ptr()
 
     @property
     def codes(self) -> torch.Tensor:
@@ -96,17 +97,21 @@ class MXTensor:
             return self._scales
         return self._whole()[self._split:].view(*self.lead, self.padded // 32)
 
+    def pointers(self) -> tuple[int, int]:
+        """Where codes and scales are now."""
+        if self._scales is None:
+            start = self._whole().data_ptr()
+            return start, start + self._split
+        codes, scales = self._forms
+        return self._given(self.home, codes), self._given(self._scales, scales)
+
     @property
     def codes_ptr(self) -> int:
-        if self._scales is None:
-            return self._whole().data_ptr()
-        return self._given(self.home, 2).data_ptr()
+        return self.pointers()[0]
 
     @property
     def scales_ptr(self) -> int:
-        if self._scales is None:
-            return self._whole().data_ptr() + self._split
-        return self._given(self._scales, 32).data_ptr()
+        return self.pointers()[1]
 
     @property
     def shape(self) -> torch.Size:
@@ -126,22 +131,22 @@ def _empty(lead, cols, like, p=None) -> MXTensor:
     # bytes of codes, the scales behind: a multiple of 64, so both are aligned
     m._split = math.prod(lead) * (m.padded // 2)
     m.home = like.new_empty(m._split // 16 * 17, dtype=torch.uint8)
-    m._scales = None
+    m._scales = m._forms = None
     return m
 
 
 def _restored(home, scales, lead, cols, p) -> MXTensor:
     """An MXTensor of the parts that a copy or a file holds."""
-    m = object.__new__(MXTensor)
-    m.cols, m.padded, m.lead, m.home, m._scales = cols, p, torch.Size(lead), home, scales
-    m._split = math.prod(lead) * (p // 2)
     if scales is not None:
-        m._given(home, 2)
-        m._given(scales, 32)
-    elif home.dtype != torch.uint8 or not home.is_contiguous() or m._whole() is not home:
-        _refuse("MXTensor: uint8 memory in one piece is wanted")
-    if cols < 0 or p % 128 or p < cols:
-        _refuse("MXTensor: a padded row is a multiple of 128 elements")
+        return MXTensor(home, scales, cols)
+    m = object.__new__(MXTensor)
+    m.cols, m.padded, m.lead, m.home = cols, p, torch.Size(lead), home
+    m._split = math.prod(lead) * (p // 2)
+    m._scales = m._forms = None
+    if (home.dtype != torch.uint8 or home.dim() != 1 or not home.is_contiguous() or cols < 0
+            or p % 128 or p < cols):
+        _refuse("MXTensor: uint8 memory in one piece is wanted, and rows padded to 128 elements")
+    m._whole()
     return m
 
 
@@ -155,8 +160,7 @@ def mx_quantize(x: torch.Tensor, stream=None) -> MXTensor:
     r, stride = _rows(x)
     q = _empty(x.shape[:-1], x.shape[-1], x)
     _b.check(_b.lib().ec_mx_quantize(r.data_ptr(), kind, r.shape[0], r.shape[1], stride,
-                                     q.codes_ptr, q.scales_ptr,
-                                     _b.current_stream(x)), "ec_mx_quantize")
+                                     *q.pointers(), _b.current_stream(x)), "ec_mx_quantize")
     return q
 
 
@@ -180,7 +184,7 @@ def mx_quantize_both(x: torch.Tensor, stream=None) -> tuple[MXTensor, MXTensor]:
     if rows and batch:
         _b.check(_b.lib().ec_mx_quantize_both(
             x.data_ptr(), kind, batch, rows, cols, batch_stride, stride,
-            a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr,
+            *a.pointers(), *b.pointers(),
             _b.current_stream(x)), "ec_mx_quantize_both")
     return a, b
 
@@ -195,7 +199,7 @@ def mx_dequantize(q: MXTensor, dtype: torch.dtype = torch.float32, stream=None) 
     lead = q.lead
     y = q.home.new_empty((*lead, q.cols), dtype=dtype)
     rows = y.numel() // q.cols
-    _b.check(_b.lib().ec_mx_dequantize(q.codes_ptr, q.scales_ptr, rows, q.cols,
+    _b.check(_b.lib().ec_mx_dequantize(*q.pointers(), rows, q.cols,
                                        y.data_ptr(), kind, q.cols, _b.current_stream(y)),
              "ec_mx_dequantize")
     return y
@@ -219,10 +223,8 @@ def mx_product(a: MXTensor, b: MXTensor, dtype: torch.dtype = torch.bfloat16,
         _refuse("mx_product: [rows, depth] and [cols, depth] on one GPU are wanted")
     rows, cols = a.lead[0], b.lead[0]
     y = a.home.new_empty((rows, cols), dtype=dtype)
-    _b.check(_b.lib().ec_mx_product(a.codes_ptr, a.scales_ptr, rows,
-                                    b.codes_ptr, b.scales_ptr, cols,
-                                    a.padded, y.data_ptr(), kind,
-                                    _b.current_stream(y)), "ec_mx_product")
+    _b.check(_b.lib().ec_mx_product(*a.pointers(), rows, *b.pointers(), cols, a.padded,
+                                    y.data_ptr(), kind,_b.current_stream(y)), "ec_mx_product")
     return y
 
 
@@ -237,8 +239,7 @@ def _linear(x, w, offsets, experts, what):
     y = x.new_empty((*x.shape[:-1], cols))
     need = L.ec_mx_linear_workspace_bytes(rows, depth, cols, experts)
     ws = w.home.new_empty(need).data_ptr() if need else None
-    _b.check(L.ec_mx_linear(r.data_ptr(), kind, rows, depth, stride, w.codes_ptr,
-                            w.scales_ptr, cols,
+    _b.check(L.ec_mx_linear(r.data_ptr(), kind, rows, depth, stride, *w.pointers(), cols,
                             offsets.data_ptr() if experts else None, experts, y.data_ptr(), ws,
                             need, _b.current_stream(x)), "ec_mx_linear")
     return y
@@ -324,9 +325,8 @@ def _quantize_groups(x, offsets, experts, rows_too=True):
     b = _empty((cols,), rows, x, int(L.ec_mx_padded_groups(rows, experts)))
     if rows:
         _b.check(L.ec_mx_quantize_groups(r.data_ptr(), TYPES[x.dtype], rows, cols, stride,
-                                         offsets.data_ptr(), experts, a.codes_ptr,
-                                         a.scales_ptr, b.codes_ptr,
-                                         b.scales_ptr, _b.current_stream(x)),
+                                         offsets.data_ptr(), experts, *a.pointers(),
+                                         *b.pointers(), _b.current_stream(x)),
                  "ec_mx_quantize_groups")
     return a, b
 
@@ -336,7 +336,7 @@ def _experts_product(a, b, offsets, dtype):
     rows = a.lead[0]
     y = a.home.new_empty((rows, cols), dtype=dtype)
     _b.check(_b.lib().ec_mx_product_experts(
-        a.codes_ptr, a.scales_ptr, rows, b.codes_ptr, b.scales_ptr, cols,
+        *a.pointers(), rows, *b.pointers(), cols,
         a.padded, offsets.data_ptr(), experts, y.data_ptr(), TYPES[dtype],
         _b.current_stream(y)), "ec_mx_product_experts")
     return y
@@ -372,7 +372,7 @@ def mx_experts_backward(dy: torch.Tensor, saved: MXLinearSaved, stream=None):
     dx = _experts_product(dr, saved.w, saved.offsets, dy.dtype)
     dw = torch.empty((experts, cols, depth), dtype=dy.dtype, device=dy.device)
     _b.check(_b.lib().ec_mx_product_tokens(
-        dc.codes_ptr, dc.scales_ptr, cols, saved.x.codes_ptr,
-        saved.x.scales_ptr, depth, saved.rows, saved.offsets.data_ptr(), experts,
+        *dc.pointers(), cols, *saved.x.pointers(), depth, saved.rows,
+        saved.offsets.data_ptr(), experts,
         dw.data_ptr(), TYPES[dy.dtype], _b.current_stream(dy)), "ec_mx_product_tokens")
     return dx, dw

@@ -71,6 +71,15 @@ def test_a_shallow_copy_shares_its_memory(make):
     assert (a.codes_ptr, a.scales_ptr, a.shape) == (q.codes_ptr, q.scales_ptr, q.shape)
 
 
+@pytest.mark.parametrize("make", [given, made])
+def test_the_tensors_that_a_stream_has_to_keep(make):
+    from error_bounded_lossy_amd import _binding
+    q = make()
+    for form in (q, copy.deepcopy(q)):
+        held = {t.untyped_storage().data_ptr() for t in _binding._tensors(form)}
+        assert held == {form.codes.untyped_storage().data_ptr(), form.scales.untyped_storage().data_ptr()}
+
+
 def test_what_a_backward_needs_copies_with_it():
     saved = mx.MXLinearSaved(made(), given(), torch.tensor([0, 2, 6], dtype=torch.int32), 6, torch.bfloat16)
     for other in (copy.deepcopy(saved), pickle.loads(pickle.dumps(saved))):
