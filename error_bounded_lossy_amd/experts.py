@@ -41,9 +41,11 @@ def expert_sort(ids: torch.Tensor, experts: int, stream=None) -> Routing:
     order, offsets = place.new_empty(n), place.new_empty(experts + 1)
     L = _b.lib()
     need = L.ec_expert_sort_workspace_bytes(n, experts)
-    ws = place.new_empty(need, dtype=torch.uint8).data_ptr() if need else None
+    # held until the call is back: before, its kernels are not all enqueued
+    ws = place.new_empty(need, dtype=torch.uint8) if need else None
     _b.check(L.ec_expert_sort(ids.data_ptr(), ids.element_size(), n, experts, order.data_ptr(),
-                              place.data_ptr(), offsets.data_ptr(), ws, need,
+                              place.data_ptr(), offsets.data_ptr(),
+                              ws.data_ptr() if need else None, need,
                               _b.current_stream(ids)), "ec_expert_sort")
     return Routing(order, place, offsets, ids.shape[0], ids.shape[1], experts)
 

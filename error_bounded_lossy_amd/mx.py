@@ -224,7 +224,7 @@ def mx_product(a: MXTensor, b: MXTensor, dtype: torch.dtype = torch.bfloat16,
     rows, cols = a.lead[0], b.lead[0]
     y = a.home.new_empty((rows, cols), dtype=dtype)
     _b.check(_b.lib().ec_mx_product(*a.pointers(), rows, *b.pointers(), cols, a.padded,
-                                    y.data_ptr(), kind,_b.current_stream(y)), "ec_mx_product")
+                                    y.data_ptr(), kind, _b.current_stream(y)), "ec_mx_product")
     return y
 
 
@@ -238,10 +238,12 @@ def _linear(x, w, offsets, experts, what):
     L = _b.lib()
     y = x.new_empty((*x.shape[:-1], cols))
     need = L.ec_mx_linear_workspace_bytes(rows, depth, cols, experts)
-    ws = w.home.new_empty(need).data_ptr() if need else None
+    # held until the call is back: before, its kernels are not all enqueued
+    ws = w.home.new_empty(need) if need else None
     _b.check(L.ec_mx_linear(r.data_ptr(), kind, rows, depth, stride, *w.pointers(), cols,
-                            offsets.data_ptr() if experts else None, experts, y.data_ptr(), ws,
-                            need, _b.current_stream(x)), "ec_mx_linear")
+                            offsets.data_ptr() if experts else None, experts, y.data_ptr(),
+                            ws.data_ptr() if need else None, need,
+                            _b.current_stream(x)), "ec_mx_linear")
     return y
 
 
