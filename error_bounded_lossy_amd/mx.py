@@ -194,7 +194,7 @@ def mx_dequantize(q: MXTensor, dtype: torch.dtype = torch.float32, stream=None) 
     if stream is not None or _b.elsewhere(q.home):
         return _b.on_stream(mx_dequantize, (q, dtype), stream)
     kind = TYPES.get(dtype)
-    if kind is None or not q.home.is_cuda or q.cols == 0:
+    if kind is None or not q.home.is_cuda or q.cols == 0 or q.padded != padded(q.cols):
         _refuse("mx_dequantize: a nonempty row on the GPU and float32, float16 or bfloat16 are wanted")
     lead = q.lead
     y = q.home.new_empty((*lead, q.cols), dtype=dtype)
@@ -219,6 +219,7 @@ def mx_product(a: MXTensor, b: MXTensor, dtype: torch.dtype = torch.bfloat16,
         return _b.on_stream(mx_product, (a, b, dtype), stream)
     kind = TYPES.get(dtype)
     if (kind is None or len(a.lead) != 1 or len(b.lead) != 1 or a.cols != b.cols or a.cols == 0
+            or not a.padded == b.padded == padded(a.cols)
             or not a.home.is_cuda or a.home.device != b.home.device):
         _refuse("mx_product: [rows, depth] and [cols, depth] on one GPU are wanted")
     rows, cols = a.lead[0], b.lead[0]
@@ -231,7 +232,8 @@ def mx_product(a: MXTensor, b: MXTensor, dtype: torch.dtype = torch.bfloat16,
 def _linear(x, w, offsets, experts, what):
     kind = _type(x, what)
     cols, depth = w.lead[-1], x.shape[-1]
-    if w.cols != depth or depth == 0 or w.home.device != x.device:
+    if (w.cols != depth or depth == 0 or w.padded != padded(depth)
+            or w.home.device != x.device):
         _refuse(f"{what}: weights [.., cols, depth] on the device of x [.., depth] are wanted")
     r, stride = _rows(x)
     rows = r.shape[0]
@@ -276,7 +278,8 @@ def mx_experts_product(a: MXTensor, b: MXTensor, offsets: torch.Tensor,
     if stream is not None or _b.elsewhere(a.home):
         return _b.on_stream(mx_experts_product, (a, b, offsets, dtype), stream)
     if (dtype not in TYPES or len(a.lead) != 1 or len(b.lead) != 2 or a.cols != b.cols
-            or a.cols == 0 or 0 in b.lead or not a.home.is_cuda
+            or a.cols == 0 or 0 in b.lead or not a.padded == b.padded == padded(a.cols)
+            or not a.home.is_cuda
             or a.home.device != b.home.device):
         _refuse("mx_experts_product: [rows, depth] and [experts, cols, depth] on one GPU are wanted")
     _offsets(offsets, b.lead[0], a.home.device, "mx_experts_product")
@@ -285,7 +288,8 @@ def mx_experts_product(a: MXTensor, b: MXTensor, offsets: torch.Tensor,
 
 class MXLinearSaved:
     """What the backward pass of a 4-bit layer needs: its input and weights along their columns
-    (17/32 of a byte an element), and for experts the offsets."""
+    (17/32 of a byte an element), and for experts the offsets.  An input's columns in groups are
+    padded by group: only the backward pass reads them."""
 
     __slots__ = ("x", "w", "offsets", "rows", "dtype")
 

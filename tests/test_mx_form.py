@@ -116,3 +116,31 @@ def test_bad_saved_state_is_refused(make):
         with pytest.raises(ec.ECError) as e:
             call(*wrong)
         assert e.value.status == ec.EC_ERR_INVALID
+
+
+class OnGPU(torch.Tensor):
+    """A tensor of the host that says it is on a GPU."""
+
+    is_cuda = True
+
+
+def test_forms_of_groups_are_not_read_as_rows(monkeypatch):
+    # rows of 300 elements in 3 groups are padded to 512 or more, plain ones to 384: a product would
+    # read the one with the other's pitch, past its end
+    from error_bounded_lossy_amd import _binding
+
+    monkeypatch.setattr(_binding, "current_stream", lambda t: 0)
+    monkeypatch.setattr(_binding, "elsewhere", lambda t: False)
+    like = torch.empty(0).as_subclass(OnGPU)
+    grouped = mx._empty((40,), 300, like, ec.lib().ec_mx_padded_groups(300, 3))
+    plain, experts = mx._empty((40,), 300, like), mx._empty((2, 40), 300, like)
+    assert grouped.padded > plain.padded and grouped.cols == plain.cols
+    monkeypatch.setattr(_binding, "lib", lambda: pytest.fail("the library was reached"))
+    offsets = torch.zeros(3, dtype=torch.int32).as_subclass(OnGPU)
+    x = torch.zeros(5, 300).as_subclass(OnGPU)
+    for call in (lambda: ec.mx_product(grouped, plain), lambda: ec.mx_product(plain, grouped),
+                 lambda: ec.mx_dequantize(grouped), lambda: ec.mx_linear(x, grouped),
+                 lambda: ec.mx_experts_product(grouped, experts, offsets)):
+        with pytest.raises(ec.ECError) as e:
+            call()
+        assert e.value.status == ec.EC_ERR_INVALID
