@@ -28,6 +28,11 @@ def elsewhere(t: torch.Tensor) -> bool:
     return device >= 0 and device != torch._C._cuda_getDevice()
 
 
+def capturing(t: torch.Tensor) -> bool:
+    """Whether calls on t, on the current stream, are being recorded into a graph."""
+    return t.get_device() >= 0 and torch.cuda.is_current_stream_capturing()
+
+
 def _tensors(v):
     if isinstance(v, torch.Tensor):
         yield v

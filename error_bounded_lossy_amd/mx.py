@@ -291,10 +291,27 @@ class MXLinearSaved:
     (17/32 of a byte an element), and for experts the offsets.  An input's columns in groups are
     padded by group: only the backward pass reads them."""
 
-    __slots__ = ("x", "w", "offsets", "rows", "dtype")
+    __slots__ = ("x", "w", "offsets", "rows", "dtype", "version")
 
     def __init__(self, x, w, offsets, rows, dtype):
         self.x, self.w, self.offsets, self.rows, self.dtype = x, w, offsets, rows, dtype
+        # The offsets are the caller's; writes to them that torch counts are found.  In a captured
+        # graph they are read at each replay, which the count knows nothing of, and torch counts
+        # none for inference tensors, which are copied.
+        self.version = None
+        if offsets is not None:
+            if offsets.is_inference():
+                self.offsets = offsets.clone()
+            elif not _b.capturing(offsets):
+                self.version = offsets._version
+
+    def same_offsets(self) -> bool:
+        return self.version is None or self.version == self.offsets._version
+
+    def __reduce__(self):
+        if not self.same_offsets():
+            _refuse("MXLinearSaved: its offsets were written to since the forward pass")
+        return MXLinearSaved, (self.x, self.w, self.offsets, self.rows, self.dtype)
 
 
 def mx_linear_forward(x: torch.Tensor, w: torch.Tensor, stream=None):
@@ -350,7 +367,8 @@ def _experts_product(a, b, offsets, dtype):
 
 def mx_experts_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, stream=None):
     """The training forward of mx_experts_linear from weights w [experts, cols, depth] of x's type;
-    the blocks of the saved columns begin anew at every expert's first row."""
+    the blocks of the saved columns begin anew at every expert's first row.  The backward pass reads
+    the same offsets: they have to keep their values until then."""
     if stream is not None or _b.elsewhere(x):
         return _b.on_stream(mx_experts_forward, (x, w, offsets), stream)
     _type(x, "mx_experts_forward")
@@ -372,6 +390,8 @@ def mx_experts_backward(dy: torch.Tensor, saved: MXLinearSaved, stream=None):
     if (saved.offsets is None or dy.dim() != 2 or dy.dtype != saved.dtype
             or dy.shape != (saved.rows, saved.w.cols) or dy.device != saved.x.device):
         _refuse("mx_experts_backward: dy [rows, cols] of the forward's type is wanted")
+    if not saved.same_offsets():
+        _refuse("mx_experts_backward: the offsets were written to since the forward pass")
     experts, depth = saved.w.lead
     cols = saved.w.cols
     dr, dc = _quantize_groups(dy, saved.offsets, experts)

@@ -1,6 +1,8 @@
 """What the binding of the 4-bit and exchange operators does around a library call, on the CPU:
 the library is a stub that looks at its arguments, and tensors pass for tensors on a GPU."""
+import copy
 import gc
+import pickle
 
 import pytest
 
@@ -14,6 +16,9 @@ class OnGPU(torch.Tensor):
     """A tensor of the host that says it is on a GPU."""
 
     is_cuda = True
+
+    def __deepcopy__(self, memo):
+        return gpu(self.as_subclass(torch.Tensor).clone())
 
 
 def gpu(t):
@@ -99,3 +104,51 @@ def test_the_workspace_of_a_sort_lives_through_the_call(stub):
     (size, alive), (none, address) = seen
     assert size == 8 * 9 * 4 and alive
     assert none == 0 and address is None
+
+
+def experts_saved(inference=False):
+    with torch.inference_mode(inference):
+        offsets = gpu(torch.tensor([0, 3, 6], dtype=torch.int32))
+        offsets.add_(0)  # a version other than a new tensor's
+        _, saved = ec.mx_experts_forward(gpu(torch.zeros(6, 64)), gpu(torch.zeros(2, 32, 64)), offsets)
+    return offsets, saved, gpu(torch.zeros(6, 32))
+
+
+# The columns are laid out by the offsets of the forward pass: with others the gradients are wrong.
+def test_offsets_written_to_after_the_forward_are_refused(stub):
+    s = stub()
+    offsets, saved, dy = experts_saved()
+    ec.mx_experts_backward(dy, saved)
+    assert s.calls[-1] == "ec_mx_product_tokens"
+    for other in (copy.copy(saved), copy.deepcopy(saved), pickle.loads(pickle.dumps(saved))):
+        ec.mx_experts_backward(dy, other)
+    calls = len(s.calls)
+    kept = copy.deepcopy(saved)
+    offsets[1] = 2
+    for call in (lambda: ec.mx_experts_backward(dy, saved), lambda: copy.deepcopy(saved)):
+        with pytest.raises(ec.ECError) as e:
+            call()
+        assert e.value.status == ec.EC_ERR_INVALID
+    assert len(s.calls) == calls
+    ec.mx_experts_backward(dy, kept)  # a copy has offsets of its own
+    # a new forward pass takes the offsets as they are now
+    ec.mx_experts_backward(dy, ec.mx_experts_forward(gpu(torch.zeros(6, 64)), gpu(torch.zeros(2, 32, 64)), offsets)[1])
+
+
+def test_offsets_that_torch_does_not_watch_are_copied(stub):
+    stub()
+    offsets, saved, dy = experts_saved(inference=True)
+    with torch.inference_mode():
+        offsets[1] = 2
+    assert saved.offsets.tolist() == [0, 3, 6]
+    ec.mx_experts_backward(dy, saved)
+
+
+def test_offsets_of_a_captured_forward_may_change(stub, monkeypatch):
+    # a graph reads them at each replay
+    stub()
+    monkeypatch.setattr(_binding, "capturing", lambda t: True, raising=False)
+    offsets, saved, dy = experts_saved()
+    offsets[1] = 2
+    ec.mx_experts_backward(dy, saved)
+    assert saved.offsets.data_ptr() == offsets.data_ptr()
