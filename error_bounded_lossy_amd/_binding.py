@@ -44,10 +44,11 @@ def _tensors(v):
 def on_stream(call, args, stream):
     """call(*args) on `stream` (None: the current one) of the first tensor's device.  Tensors from
     other streams stay allocated until the work on this one is done."""
-    first = next(t for a in args for t in _tensors(a))
-    if not first.is_cuda:
+    first = next((t for a in args for t in _tensors(a)), None)
+    if first is None or not first.is_cuda:
         raise ECError(EC_ERR_INVALID, f"{call.__name__}: tensors on the GPU are wanted")
-    if stream is not None and stream.device != first.device:
+    if stream is not None and (not hasattr(stream, "stream_id")
+                               or getattr(stream, "device", None) != first.device):
         raise ECError(EC_ERR_INVALID, f"{call.__name__}: a stream of the tensors' device is wanted")
     with torch.cuda.device(first.device), torch.cuda.stream(stream):
         out = call(*args)

@@ -152,3 +152,26 @@ def test_offsets_of_a_captured_forward_may_change(stub, monkeypatch):
     offsets[1] = 2
     ec.mx_experts_backward(dy, saved)
     assert saved.offsets.data_ptr() == offsets.data_ptr()
+
+
+# ---------------------------------------------------------------- streams
+
+
+CALLS = [lambda s: ec.mx_quantize(gpu(torch.zeros(4, 64)), stream=s),
+         lambda s: ec.mx_product(form(4, 64), form(5, 64), stream=s),
+         lambda s: ec.expert_sort(gpu(torch.zeros(4, 2, dtype=torch.int32)), 4, stream=s)]
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("stream", [7, object(), "stream", torch.device("cpu"), gpu(torch.zeros(1))], ids=lambda v: type(v).__name__)
+def test_what_is_no_stream_is_refused(call, stream):
+    with pytest.raises(ec.ECError) as e:
+        call(stream)
+    assert e.value.status == ec.EC_ERR_INVALID
+
+
+def test_calls_without_a_tensor_are_refused():
+    for call in (ec.mx_quantize, ec.mx_quantize_both, ec.mx_dequantize):
+        with pytest.raises(ec.ECError) as e:
+            call(None, stream=object())
+        assert e.value.status == ec.EC_ERR_INVALID
