@@ -51,9 +51,10 @@ def on_stream(call, args, stream):
                                or getattr(stream, "device", None) != first.device):
         raise ECError(EC_ERR_INVALID, f"{call.__name__}: a stream of the tensors' device is wanted")
     with torch.cuda.device(first.device), torch.cuda.stream(stream):
-        out = call(*args)
-        if stream is not None:
-            for a in args:
-                for t in _tensors(a):
-                    t.record_stream(stream)
-    return out
+        try:
+            return call(*args)
+        finally:  # a call that failed may have enqueued a part of its work
+            if stream is not None:
+                for a in args:
+                    for t in _tensors(a):
+                        t.record_stream(stream)

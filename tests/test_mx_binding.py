@@ -175,3 +175,31 @@ def test_calls_without_a_tensor_are_refused():
         with pytest.raises(ec.ECError) as e:
             call(None, stream=object())
         assert e.value.status == ec.EC_ERR_INVALID
+
+
+# A call that fails may have enqueued a part of its work, which reads its inputs.
+@pytest.mark.parametrize("fails", [False, True])
+def test_inputs_stay_for_another_stream_also_when_a_call_fails(monkeypatch, fails):
+    import contextlib
+
+    recorded = []
+
+    class Input(OnGPU):
+        def record_stream(self, stream):
+            recorded.append(stream)
+
+    class Stream:
+        device, stream_id = torch.device("cpu"), 1
+
+    def call(x):
+        if fails:
+            raise ec.ECError(ec.EC_ERR_DEVICE, "call")
+        return x
+
+    for name in ("device", "stream"):
+        monkeypatch.setattr(torch.cuda, name, lambda *a: contextlib.nullcontext())
+    s = Stream()
+    x = torch.zeros(3).as_subclass(Input)
+    with (pytest.raises(ec.ECError) if fails else contextlib.nullcontext()):
+        _binding.on_stream(call, (x,), s)
+    assert recorded == [s]
