@@ -13,6 +13,11 @@ from . import _binding as _b
 from .mx import TYPES, MXTensor, _empty, _refuse, _type
 
 
+def _ints(t, shape) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.shape == shape
+            and t.is_contiguous())
+
+
 class Routing:
     """Where the choices ids [tokens, choices] go: order, int32 [tokens * choices], the flat choice
     of each sorted row (-1 past the last); place, int32 [tokens, choices], the row of each choice
@@ -21,6 +26,14 @@ class Routing:
     __slots__ = ("order", "place", "offsets", "tokens", "choices", "experts")
 
     def __init__(self, order, place, offsets, tokens, choices, experts):
+        if not (_ints(order, (tokens * choices,)) and _ints(place, (tokens, choices))
+                and _ints(offsets, (experts + 1,)) and choices > 0 and experts > 0
+                and order.device == place.device == offsets.device):
+            _refuse("Routing: int32 order [tokens * choices], place [tokens, choices] and "
+                    "offsets [experts + 1], contiguous and on one device, are wanted")
+        self._set(order, place, offsets, tokens, choices, experts)
+
+    def _set(self, order, place, offsets, tokens, choices, experts):
         self.order, self.place, self.offsets = order, place, offsets
         self.tokens, self.choices, self.experts = tokens, choices, experts
 
@@ -47,7 +60,9 @@ def expert_sort(ids: torch.Tensor, experts: int, stream=None) -> Routing:
                               place.data_ptr(), offsets.data_ptr(),
                               ws.data_ptr() if need else None, need,
                               _b.current_stream(ids)), "ec_expert_sort")
-    return Routing(order, place, offsets, ids.shape[0], ids.shape[1], experts)
+    r = object.__new__(Routing)  # of these arrays there is nothing to check
+    r._set(order, place, offsets, ids.shape[0], ids.shape[1], experts)
+    return r
 
 
 def _tokens(x, r, what):

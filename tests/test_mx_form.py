@@ -144,3 +144,34 @@ def test_forms_of_groups_are_not_read_as_rows(monkeypatch):
         with pytest.raises(ec.ECError) as e:
             call()
         assert e.value.status == ec.EC_ERR_INVALID
+
+
+# ---------------------------------------------------------------- routings
+
+
+def routing(**other):
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    parts = {"order": i32(12), "place": i32(6, 2), "offsets": i32(5), "tokens": 6, "choices": 2, "experts": 4}
+    return ec.Routing(**{**parts, **other})
+
+
+# Its arrays go to the device as they are: with another type or size the exchange would read past them.
+@pytest.mark.parametrize("wrong", [
+    {"place": torch.zeros(6, 2, dtype=torch.int64)}, {"place": torch.zeros(5, 2, dtype=torch.int32)},
+    {"place": torch.zeros(12, dtype=torch.int32)}, {"place": torch.zeros(2, 6, dtype=torch.int32).t()},
+    {"offsets": torch.zeros(4, dtype=torch.int32)}, {"offsets": torch.zeros(5)},
+    {"offsets": torch.zeros(10, dtype=torch.int32)[::2]}, {"offsets": torch.zeros(5, dtype=torch.int32, device="meta")},
+    {"order": torch.zeros(11, dtype=torch.int32)}, {"order": torch.zeros(12, dtype=torch.int64)},
+    {"tokens": 7}, {"choices": 3}, {"choices": 0}, {"experts": 5}, {"experts": 0}, {"place": None}],
+    ids=lambda w: "-".join(f"{k}" for k in w))
+def test_routings_of_other_arrays_are_refused(wrong):
+    routing()
+    with pytest.raises(ec.ECError) as e:
+        routing(**wrong)
+    assert e.value.status == ec.EC_ERR_INVALID
+
+
+def test_routings_copy_with_their_arrays():
+    r = routing()
+    for other in (copy.deepcopy(r), pickle.loads(pickle.dumps(r))):
+        assert other.place.data_ptr() != r.place.data_ptr() and other.experts == 4
