@@ -173,7 +173,7 @@ struct At {
   uint32_t lane, lanes;
 };
 __device__ __forceinline__ At at(const Shape& s) {
-  return {(uint64_t)blockIdx.x * (kThreads >> s.shift) + (threadIdx.x >> s.shift),
+  return {(uint64_t)block_number() * (kThreads >> s.shift) + (threadIdx.x >> s.shift),
           threadIdx.x & ((1u << s.shift) - 1), 1u << s.shift};
 }
 
@@ -463,7 +463,7 @@ ec_status ec_expert_dispatch(const void* x, int type, uint64_t tokens, uint64_t 
     return EC_ERR_INVALID;
   const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
                            tokens * choices * cols * type_bytes(type));
-  BY_TYPE(type, hipLaunchKernelGGL((expert_dispatch<T>), dim3((uint32_t)blocks_of(s)),
+  BY_TYPE(type, hipLaunchKernelGGL((expert_dispatch<T>), grid_of(blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)x, s, place,
                                    offsets, experts, (T*)xs));
   return launched();
@@ -480,7 +480,7 @@ ec_status ec_expert_dispatch_mx(const void* x, int type, uint64_t tokens, uint64
     return EC_ERR_INVALID;
   const Shape s = shape_of(tokens, cols, choices, (uint32_t)(ec_mx_padded(cols) / 8), 2,
                            0);
-  BY_TYPE(type, hipLaunchKernelGGL((expert_dispatch_mx<T>), dim3((uint32_t)blocks_of(s)),
+  BY_TYPE(type, hipLaunchKernelGGL((expert_dispatch_mx<T>), grid_of(blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)x, s, place,
                                    offsets, experts, (uint8_t*)codes, (uint8_t*)scales));
   return launched();
@@ -495,7 +495,7 @@ ec_status ec_expert_dispatch_backward(const void* dxs, int type, uint64_t tokens
     return EC_ERR_INVALID;
   const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
                            tokens * cols * type_bytes(type));
-  BY_TYPE(type, hipLaunchKernelGGL((expert_gather<T, false, 2>), dim3((uint32_t)blocks_of(s)),
+  BY_TYPE(type, hipLaunchKernelGGL((expert_gather<T, false, 2>), grid_of(blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)dxs, s, place,
                                    (const void*)nullptr, 0, (T*)dx));
   return launched();
@@ -513,7 +513,7 @@ ec_status ec_expert_combine(const void* ys, int type, uint64_t tokens, uint64_t 
     return EC_ERR_INVALID;
   const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
                            tokens * cols * type_bytes(type));
-  BY_TYPE(type, hipLaunchKernelGGL((expert_gather<T, true, 2>), dim3((uint32_t)blocks_of(s)),
+  BY_TYPE(type, hipLaunchKernelGGL((expert_gather<T, true, 2>), grid_of(blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)ys, s, place,
                                    weights, wtype, (T*)y));
   return launched();
@@ -534,7 +534,7 @@ ec_status ec_expert_combine_backward(const void* dy, const void* ys, int type, u
     return EC_ERR_INVALID;
   const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
                            tokens * choices * cols * b);
-  BY_TYPE(type, hipLaunchKernelGGL((expert_combine_back<T, 2>), dim3((uint32_t)blocks_of(s)),
+  BY_TYPE(type, hipLaunchKernelGGL((expert_combine_back<T, 2>), grid_of(blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)dy,
                                    (const T*)ys, s, place, weights, wtype, offsets, experts,
                                    (T*)dys, dweights));

@@ -30,7 +30,7 @@ __global__ __launch_bounds__(kThreads) void mx_rows(const T* __restrict__ x, uin
                                                     uint32_t col_tiles, uint8_t* codes,
                                                     uint8_t* scales) {
   const uint32_t tid = threadIdx.x, ty = kThreads >> tx_shift;
-  const uint32_t ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;
+  const uint32_t block = block_number(), ct = block % col_tiles, rt = block / col_tiles;
   const uint32_t chunk = (ct << tx_shift) + (tid & ((1u << tx_shift) - 1));
   const uint64_t row0 = (uint64_t)rt * ty * ROWS + (tid >> tx_shift);
   if (chunk * 8 >= padded) return;  // whole quads of lanes: padded is a multiple of 128
@@ -84,8 +84,8 @@ __global__ __launch_bounds__(kThreads, 2) void mx_both(
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t cg = lane & 15, rb = lane >> 4;
   const uint32_t pairs = (col_tiles + 1) / 2;
-  const uint32_t ct = 2 * (blockIdx.x % pairs) + (wave >> 1);
-  const uint64_t rt = 2 * (uint64_t)(blockIdx.x / pairs) + (wave & 1);
+  const uint32_t block = block_number(), ct = 2 * (block % pairs) + (wave >> 1);
+  const uint64_t rt = 2 * (uint64_t)(block / pairs) + (wave & 1);
   if (ct >= col_tiles || rt >= row_tiles) return;
   uint64_t first = rt * 128, last = rows;  // this wave's rows
   if (offsets) {
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(kThreads) void mx_values(const uint8_t* __restrict_
                                                       bool past) {
   constexpr uint32_t E = 16 / sizeof(T);
   const uint32_t tid = threadIdx.x, ty = kThreads >> tx_shift;
-  const uint32_t ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;
+  const uint32_t block = block_number(), ct = block % col_tiles, rt = block / col_tiles;
   const uint32_t c0 = ((ct << tx_shift) + (tid & ((1u << tx_shift) - 1))) * E;
   const uint64_t row0 = (uint64_t)rt * ty * ROWS + (tid >> tx_shift);
   if (c0 >= cols) return;
@@ -331,13 +331,13 @@ ec_status rows_of(const void* x, uint64_t rows, uint64_t cols, uint64_t stride, 
   const uint64_t tiles = ceil_div(padded / 8, 1ull << sh), ty = kThreads >> sh;
   const uint32_t per = many(rows * (padded / 8)) ? 4 : 1;
   const uint64_t blocks = tiles * ceil_div(rows, ty * per);
-  if (blocks > 0x7fffffffull) return EC_ERR_UNSUPPORTED;
+  if (blocks > kMostBlocks) return EC_ERR_UNSUPPORTED;
   if (per == 4)
-    hipLaunchKernelGGL((mx_rows<T, 4>), dim3((uint32_t)blocks), dim3(kThreads), 0, s,
+    hipLaunchKernelGGL((mx_rows<T, 4>), grid_of(blocks), dim3(kThreads), 0, s,
                        (const T*)x, rows, (uint32_t)cols, stride, padded, sh, (uint32_t)tiles,
                        (uint8_t*)codes, (uint8_t*)scales);
   else
-    hipLaunchKernelGGL((mx_rows<T, 1>), dim3((uint32_t)blocks), dim3(kThreads), 0, s,
+    hipLaunchKernelGGL((mx_rows<T, 1>), grid_of(blocks), dim3(kThreads), 0, s,
                        (const T*)x, rows, (uint32_t)cols, stride, padded, sh, (uint32_t)tiles,
                        (uint8_t*)codes, (uint8_t*)scales);
   return launched();
@@ -353,8 +353,8 @@ ec_status both_of(const void* x, uint64_t batch, uint64_t rows, uint64_t cols,
   const uint32_t ct = (uint32_t)ceil_div(rc ? pc : cols, width);
   const uint64_t rt = pr / 128;
   const uint64_t blocks = ceil_div(ct, 2) * ceil_div(rt, 2);
-  if (blocks > 0x7fffffffull) return EC_ERR_UNSUPPORTED;
-  const dim3 grid((uint32_t)blocks, 1, (uint32_t)batch), block(kThreads);
+  if (blocks > kMostBlocks) return EC_ERR_UNSUPPORTED;
+  const dim3 grid = grid_of(blocks, (uint32_t)batch), block(kThreads);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, block, 0, s, (const T*)x, rows, (uint32_t)cols, batch_stride,
                        stride, offsets, groups, ct, rt, (uint8_t*)rc, (uint8_t*)rs, (uint8_t*)cc,
@@ -374,14 +374,14 @@ ec_status values_of(const void* codes, const void* scales, uint64_t rows, uint64
   const uint64_t tiles = ceil_div(ceil_div(cols, E), 1ull << sh), ty = kThreads >> sh;
   const uint32_t per = many(rows * (padded / E)) ? 4 : 1;
   const uint64_t blocks = tiles * ceil_div(rows, ty * per);
-  if (blocks > 0x7fffffffull) return EC_ERR_UNSUPPORTED;
+  if (blocks > kMostBlocks) return EC_ERR_UNSUPPORTED;
   const bool past = past_caches(rows * cols * sizeof(T));
   if (per == 4)
-    hipLaunchKernelGGL((mx_values<T, 4>), dim3((uint32_t)blocks), dim3(kThreads), 0, s,
+    hipLaunchKernelGGL((mx_values<T, 4>), grid_of(blocks), dim3(kThreads), 0, s,
                        (const uint8_t*)codes, (const uint8_t*)scales, rows, (uint32_t)cols, padded,
                        (T*)y, stride, sh, (uint32_t)tiles, past);
   else
-    hipLaunchKernelGGL((mx_values<T, 1>), dim3((uint32_t)blocks), dim3(kThreads), 0, s,
+    hipLaunchKernelGGL((mx_values<T, 1>), grid_of(blocks), dim3(kThreads), 0, s,
                        (const uint8_t*)codes, (const uint8_t*)scales, rows, (uint32_t)cols, padded,
                        (T*)y, stride, sh, (uint32_t)tiles, past);
   return launched();

@@ -24,6 +24,20 @@ inline bool type_known(int type) {
 inline bool aligned(const void* p, size_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 inline uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
+// A launch has less than 2^32 threads along x: with up to 512 threads a
+// workgroup, their numbers past 22 bits go on along y. The last row may have
+// more than there is work for: kernels check their numbers anyhow.
+constexpr uint32_t kGridBits = 22;
+constexpr uint64_t kMostBlocks = 0x7fffffffull;
+inline dim3 grid_of(uint64_t blocks, uint32_t z = 1) {
+  const uint64_t wide = 1ull << kGridBits;
+  return blocks <= wide ? dim3((uint32_t)blocks, 1, z)
+                        : dim3((uint32_t)wide, (uint32_t)ceil_div(blocks, wide), z);
+}
+__device__ __forceinline__ uint32_t block_number() {
+  return blockIdx.y << kGridBits | blockIdx.x;
+}
+
 template <typename To, typename From>
 __device__ __forceinline__ To bits_as(From v) {
   static_assert(sizeof(To) == sizeof(From), "same size");
@@ -214,7 +228,7 @@ __device__ __forceinline__ uint32_t max_of_8_lanes(uint32_t v) {
 // run of consecutive items, of each of `sets` sets in turn.  The grid is
 // `items` rounded up to 8, times sets.
 __device__ __forceinline__ bool dealt(uint32_t items, uint32_t sets, uint32_t& t, uint32_t& set) {
-  const uint32_t run = (items + 7) / 8, i = blockIdx.x >> 3;
+  const uint32_t run = (items + 7) / 8, i = block_number() >> 3;
   set = i / run;
   t = (blockIdx.x & 7) * run + (i - set * run);
   return set < sets && t < items;

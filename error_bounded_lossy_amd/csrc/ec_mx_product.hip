@@ -443,15 +443,16 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void mx_few(const Few p) {
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t waves = blockDim.x >> 6;
   const uint32_t r = lane & 15, g = lane >> 4;
-  const uint32_t tn = blockIdx.x % p.n_tiles;
+  const uint32_t block = block_number(), tn = block % p.n_tiles;
   const uint32_t n0 = tn * kFewCols * NT;
+  if (!p.experts && block >= p.n_tiles) return;
   uint64_t row0 = 0;
   uint32_t here = (uint32_t)p.rows;
   T* y = (T*)p.y;
   const uint8_t *bc = p.b.codes, *bs = p.b.scales;
   if (p.experts) {
     const GroupTile gt =
-        find_tile(p.offsets, p.experts, p.rows, p.shift, blockIdx.x / p.n_tiles);
+        find_tile(p.offsets, p.experts, p.rows, p.shift, block / p.n_tiles);
     const uint64_t skip = (uint64_t)gt.local << p.shift;
     if (gt.group == p.experts) {  // rows of no group: zeros
       const int64_t f = p.offsets[p.experts];
@@ -576,10 +577,10 @@ ec_status tiles_as(Product p, hipStream_t s) {
   // groups round up each, and the rows of no group once more
   if (MODE == kExperts) m += (p.experts < p.rows ? p.experts : p.rows) + 1;
   const uint64_t tiles = ceil_div(m * p.n_tiles, 8) * 8 * (MODE == kTokens ? p.experts : 1);
-  if (tiles > 0x7fffffffull) return EC_ERR_UNSUPPORTED;
+  if (tiles > kMostBlocks) return EC_ERR_UNSUPPORTED;
   p.m_tiles = (uint32_t)m;
   p.past = past_caches(p.rows * p.cols * sizeof(T) * (MODE == kTokens ? p.experts : 1));
-  hipLaunchKernelGGL((mx_tiles<FM, FN, T, MODE>), dim3((uint32_t)tiles),
+  hipLaunchKernelGGL((mx_tiles<FM, FN, T, MODE>), grid_of(tiles),
                      dim3(256), 0, s, p);
   return launched();
 }
@@ -653,14 +654,14 @@ ec_status few_as(Few p, bool quantize, uint32_t waves, hipStream_t s) {
   const uint64_t m =
       p.experts ? ceil_div(p.rows, p.held) + (p.experts < p.rows ? p.experts : p.rows) + 1 : 1;
   const uint64_t blocks = p.n_tiles * m;
-  if (blocks > 0x7fffffffull) return EC_ERR_UNSUPPORTED;
+  if (blocks > kMostBlocks) return EC_ERR_UNSUPPORTED;
   const uint32_t rows = p.rows < p.held ? (uint32_t)p.rows : p.held;  // what LDS has to hold
   const uint32_t lds = quantize ? rows * (p.depth / 2 + 16 + p.depth / 32) : 0;
   if (quantize)
-    hipLaunchKernelGGL((mx_few<T, true, NT, SETS>), dim3((uint32_t)blocks), dim3(64 * waves), lds,
+    hipLaunchKernelGGL((mx_few<T, true, NT, SETS>), grid_of(blocks), dim3(64 * waves), lds,
                        s, p);
   else
-    hipLaunchKernelGGL((mx_few<T, false, NT, SETS>), dim3((uint32_t)blocks), dim3(64 * waves), lds,
+    hipLaunchKernelGGL((mx_few<T, false, NT, SETS>), grid_of(blocks), dim3(64 * waves), lds,
                        s, p);
   return launched();
 }
