@@ -475,7 +475,7 @@ ec_status ec_expert_dispatch_mx(const void* x, int type, uint64_t tokens, uint64
   ec_status st = check(type, tokens, cols, choices);
   if (st == EC_OK) st = check_experts(experts);
   if (st != EC_OK || tokens == 0) return st;
-  if (!fine(x, type_bytes(type)) || !fine(codes, 16) || !fine(scales, 16) || !fine(place, 4) ||
+  if (!fine(x, type_bytes(type)) || !written_ok(codes, scales) || !fine(place, 4) ||
       !fine(offsets, 4))
     return EC_ERR_INVALID;
   const Shape s = shape_of(tokens, cols, choices, (uint32_t)(ec_mx_padded(cols) / 8), 2,

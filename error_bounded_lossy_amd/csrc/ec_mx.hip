@@ -387,17 +387,13 @@ ec_status values_of(const void* codes, const void* scales, uint64_t rows, uint64
   return launched();
 }
 
-bool form_ok(const void* codes, const void* scales) {
-  return codes && scales && aligned(codes, 16) && aligned(scales, 16);
-}
-
 ec_status both(const void* x, int type, uint64_t batch, uint64_t rows, uint64_t cols,
                uint64_t batch_stride, uint64_t stride, const int32_t* offsets, uint32_t groups,
                void* rc, void* rs, void* cc, void* cs, void* stream) {
   if (!type_known(type) || cols == 0 || stride < cols || (!rc) != (!rs) || (!cc) != (!cs) ||
       (!rc && !cc))
     return EC_ERR_INVALID;
-  if ((rc && !form_ok(rc, rs)) || (cc && !form_ok(cc, cs))) return EC_ERR_INVALID;
+  if ((rc && !written_ok(rc, rs)) || (cc && !written_ok(cc, cs))) return EC_ERR_INVALID;
   if (!shape_ok(rows, cols) || !shape_ok(cols, rows) || batch > EC_MX_MAX_GROUPS)
     return EC_ERR_UNSUPPORTED;
   if (batch * rows == 0) return EC_OK;
@@ -432,7 +428,7 @@ ec_status ec_mx_quantize(const void* x, int type, uint64_t rows, uint64_t cols, 
   if (!type_known(type) || cols == 0 || stride < cols) return EC_ERR_INVALID;
   if (!shape_ok(rows, cols)) return EC_ERR_UNSUPPORTED;
   if (rows == 0) return EC_OK;
-  if (!x || !aligned(x, type_bytes(type)) || !form_ok(codes, scales)) return EC_ERR_INVALID;
+  if (!x || !aligned(x, type_bytes(type)) || !written_ok(codes, scales)) return EC_ERR_INVALID;
   hipStream_t s = (hipStream_t)stream;
   switch (type) {
     case EC_TYPE_F32: return rows_of<float>(x, rows, cols, stride, codes, scales, s);
@@ -464,7 +460,7 @@ ec_status ec_mx_dequantize(const void* codes, const void* scales, uint64_t rows,
   if (!type_known(type) || cols == 0 || stride < cols) return EC_ERR_INVALID;
   if (!shape_ok(rows, cols)) return EC_ERR_UNSUPPORTED;
   if (rows == 0) return EC_OK;
-  if (!form_ok(codes, scales) || !y || !aligned(y, type_bytes(type))) return EC_ERR_INVALID;
+  if (!read_ok(codes, scales) || !y || !aligned(y, type_bytes(type))) return EC_ERR_INVALID;
   hipStream_t s = (hipStream_t)stream;
   switch (type) {
     case EC_TYPE_F32: return values_of<float>(codes, scales, rows, cols, y, stride, s);

@@ -22,6 +22,14 @@ inline bool type_known(int type) {
   return type == EC_TYPE_F32 || type == EC_TYPE_F16 || type == EC_TYPE_BF16;
 }
 inline bool aligned(const void* p, size_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+// Codes and scales that are written, and that are read: rows of scales start
+// at multiples of 4 bytes, so a part of a tensor's rows may.
+inline bool written_ok(const void* codes, const void* scales) {
+  return codes && scales && aligned(codes, 16) && aligned(scales, 16);
+}
+inline bool read_ok(const void* codes, const void* scales) {
+  return codes && scales && aligned(codes, 16) && aligned(scales, 4);
+}
 inline uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
 // A launch has less than 2^32 threads along x: with up to 512 threads a

@@ -686,10 +686,6 @@ ec_status few(const Few& p, int type, bool quantize, hipStream_t s) {
   }
 }
 
-bool form_ok(const void* codes, const void* scales) {
-  return codes && scales && aligned(codes, 16) && aligned(scales, 16);
-}
-
 ec_status check(const void* a, const void* sa, uint64_t rows, const void* b, const void* sb,
                 uint64_t cols, uint64_t depth, const void* y, int type) {
   if (!type_known(type) || cols == 0 || depth % 128 != 0) return EC_ERR_INVALID;
@@ -697,7 +693,7 @@ ec_status check(const void* a, const void* sa, uint64_t rows, const void* b, con
     return EC_ERR_UNSUPPORTED;
   if (rows == 0) return EC_OK;
   if (!y || !aligned(y, type_bytes(type))) return EC_ERR_INVALID;
-  if (depth && (!form_ok(b, sb) || !form_ok(a, sa))) return EC_ERR_INVALID;
+  if (depth && (!read_ok(b, sb) || !read_ok(a, sa))) return EC_ERR_INVALID;
   return EC_OK;
 }
 
@@ -814,7 +810,7 @@ ec_status ec_mx_linear(const void* x, int type, uint64_t rows, uint64_t depth, u
     return EC_ERR_UNSUPPORTED;
   if (rows == 0) return EC_OK;
   if (!x || !aligned(x, type_bytes(type)) || !y || !aligned(y, type_bytes(type)) ||
-      !form_ok(w_codes, w_scales) || !aligned(offsets, 4) || !aligned(workspace, 16))
+      !read_ok(w_codes, w_scales) || !aligned(offsets, 4) || !aligned(workspace, 16))
     return EC_ERR_INVALID;
   const size_t need = ec_mx_linear_workspace_bytes(rows, depth, cols, experts);
   if (need && !workspace) return EC_ERR_INVALID;

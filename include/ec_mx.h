@@ -29,8 +29,9 @@
  * Conventions: as in ec.h (status codes, stream handles, caller-owned device
  * memory; calls enqueue kernels and never allocate or synchronize, so they
  * can be captured into graphs).  Inputs and outputs x, y need the alignment
- * of their element; codes and scales have to be 16-byte aligned.  Strides
- * are in elements.  Results do not depend on the run: no sum's order is left
+ * of their element; codes have to be 16-byte aligned, scales that are written
+ * 16-byte and scales that are read 4-byte aligned: any rows of a tensor, in
+ * a row, are a tensor to read.  Strides are in elements.  Results do not depend on the run: no sum's order is left
  * to chance.
  */
 #ifndef EC_MX_H

@@ -156,3 +156,16 @@ def test_binding_refuses_tensors_of_the_host():
                                 (q.codes.int(), q.scales, 64), (q.codes[:3], q.scales, 64)):
         with pytest.raises(ec.ECError):
             ec.MXTensor(codes, scales, cols)
+
+
+def test_scales_that_are_read_start_at_words(L):
+    # (4-byte aligned ones are taken: a part of a tensor's rows, tested on the GPU)
+    for off in (1, 2, 3, 6):
+        assert L.ec_mx_dequantize(F, F + off, 1, 8, F, BF16, 8, None) == INVALID
+        assert L.ec_mx_product(F, F + off, 1, F, F, 8, 128, F, BF16, None) == INVALID
+        assert L.ec_mx_product(F, F, 1, F, F + off, 8, 128, F, BF16, None) == INVALID
+        assert L.ec_mx_linear(F, BF16, 1, 64, 64, F, F + off, 8, None, 0, F, None, 0, None) == INVALID
+    for off in (4, 8, 12):  # codes, and scales that are written
+        assert L.ec_mx_dequantize(F + off, F, 1, 8, F, BF16, 8, None) == INVALID
+        assert L.ec_mx_quantize(F, BF16, 1, 8, 8, F, F + off, None) == INVALID
+        assert L.ec_expert_dispatch_mx(F, BF16, 1, 8, F, 2, F, 4, F, F + off, None) == INVALID
