@@ -133,6 +133,8 @@ def lib():
         ("ec_mx_product", st, (vp, vp, u64, vp, vp, u64, u64, vp, i, vp)),
         ("ec_mx_product_experts", st, (vp, vp, u64, vp, vp, u64, u64, vp, u32, vp, i, vp)),
         ("ec_mx_product_tokens", st, (vp, vp, u64, vp, vp, u64, u64, vp, u32, vp, i, vp)),
+        ("ec_mx_product_tile", u32, (u64, u64, u64, i, u32, u64)),
+        ("ec_mx_product_rows_first", u64, (u64, u64, u64, i)),
         ("ec_mx_linear_workspace_bytes", sz, (u64, u64, u64, u32)),
         ("ec_mx_linear", st, (vp, i, u64, u64, u64, vp, vp, u64, vp, u32, vp, vp, sz, vp)),
         ("ec_expert_sort_workspace_bytes", sz, (u64, u32)),

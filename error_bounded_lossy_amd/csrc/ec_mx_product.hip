@@ -594,46 +594,85 @@ ec_status tiles_as(Product p, hipStream_t s) {
 // and 3.5 and 5.5 more a round of 512.  Finding a group's rows adds 5 to a
 // round of large ones and tokens' parts 3 (16 groups, 16384 x 2048 x 2048:
 // large 62 and 85 us, small 59 and 79; tokens of 4 groups, 4096 x 4096 x 4096:
-// large 71, small 77).  Costs in us times 1024.
+// large 71, small 77).  A round's stores are half of what does not grow with
+// the contraction: a dense product in fp32 stores twice as much, and costs 17
+// and 9, and 5 and 5.5, there (8192 x 8192 outputs, contractions of 512, 2048,
+// 4096 and 8192: large 94, 143, 216, 362 us, small 62, 117, 207, 409; experts
+// and tokens in fp32 are within 9% of the better tile with the costs of bf16).
+// Costs in us times 1024.
 //
 // Tiles of 64 where fewer than 128 of 128 would run: 1024 x 4096 x 4096 takes
 // 22 us with tiles of 128 and 30 with 64, 64 x 4096 x 4096 10.4 with 64.
 struct Tiles {
   uint64_t large, small;            // how many
   uint64_t cost_large, cost_small;  // too few large ones: more than anything
+  uint64_t round_small;             // what 512 small ones cost
 };
-Tiles tiles_for(int mode, uint64_t rows, uint64_t cols, uint64_t depth, uint64_t groups) {
+Tiles tiles_for(int mode, uint64_t rows, uint64_t cols, uint64_t depth, uint64_t groups,
+                size_t bytes) {
   const uint64_t extra = mode == kExperts ? groups / 2 : 0;  // half a tile more for each
   const uint64_t sets = mode == kTokens ? groups : 1;
   Tiles t;
   t.large = (ceil_div(rows, 256) + extra) * ceil_div(cols, 256) * sets;
   t.small = (ceil_div(rows, 128) + extra) * ceil_div(cols, 128) * sets;
-  const uint64_t start = mode == kDense ? 8 : mode == kExperts ? 13 : 11;
-  t.cost_large = t.large < 192 ? ~0ull >> 1 : ceil_div(t.large, 256) * (start * 1024 + depth * 8);
-  t.cost_small = ceil_div(t.small, 512) * (3584 + depth * 11 / 2);
+  const bool twice = mode == kDense && bytes == 4;
+  const uint64_t start = mode == kDense ? (twice ? 17 : 8) : mode == kExperts ? 13 : 11;
+  t.round_small = (twice ? 5120 : 3584) + depth * 11 / 2;
+  t.cost_large = t.large < 192 ? ~0ull >> 1
+                               : ceil_div(t.large, 256) * (start * 1024 + depth * (twice ? 9 : 8));
+  t.cost_small = ceil_div(t.small, 512) * t.round_small;
   return t;
+}
+
+// Rows and columns of a tile.
+uint32_t side_of(const Tiles& t) {
+  return t.cost_large <= t.cost_small ? 256 : t.small >= 128 ? 128 : 64;
+}
+// The contraction that the costs go by: a stored row, or an expert's mean part of it.
+uint64_t mean_depth(int mode, uint64_t depth, uint64_t tokens, uint32_t experts) {
+  return mode == kTokens ? tokens / experts : depth;
 }
 
 template <typename T, int MODE>
 ec_status tiles_of(const Product& p, hipStream_t s) {
-  const Tiles t = tiles_for(MODE, p.rows, p.cols,
-                            MODE == kTokens ? p.tokens / p.experts : p.depth, p.experts);
-  if (t.cost_large <= t.cost_small) return tiles_as<4, 4, T, MODE>(p, s);
-  if (t.small >= 128) return tiles_as<2, 2, T, MODE>(p, s);
-  return tiles_as<1, 1, T, MODE>(p, s);
+  switch (side_of(tiles_for(MODE, p.rows, p.cols,
+                            mean_depth(MODE, p.depth, p.tokens, p.experts), p.experts,
+                            sizeof(T)))) {
+    case 256: return tiles_as<4, 4, T, MODE>(p, s);
+    case 128: return tiles_as<2, 2, T, MODE>(p, s);
+    default: return tiles_as<1, 1, T, MODE>(p, s);
+  }
+}
+
+// What a product of under 256 rows costs, by the way that it takes (us, contractions
+// of 1024, 4096, 8192): 16 rows by 4096 columns 3.7, 5.6, 8.8, by 57344 11.6, 35, 82;
+// 250 by 4096 (256 tiles of 64) 4.6, 8.8, 14, by 16384 (256 of 128) 7.2, 17, 27, by
+// 57344 (224 of 256) 18.5, 43, 85.
+uint64_t cost_of_few(uint64_t rows, uint64_t cols, uint64_t depth, size_t bytes) {
+  if (rows <= kFewRows) return 3 * 1024 + (cols * depth * 10 >> 16);
+  const Tiles t = tiles_for(kDense, rows, cols, depth, 1, bytes);
+  if (t.cost_large <= t.cost_small) return t.cost_large + 4 * 1024;
+  if (t.small >= 128) return ceil_div(t.small, 256) * (3 * 1024 + depth * 3);
+  return ceil_div(ceil_div(rows, 64) * ceil_div(cols, 64), 256) * (3 * 1024 + depth * 3 / 2);
 }
 
 // Rows (a multiple of 256) whose large tiles go first where the rest, which
-// would begin another round, goes to a launch of its own: under 256 rows take
-// 8 to 10 us by 4096 x 4096, a round of large tiles 43 (4100 rows: 50, with
-// tiles of 128 65, large ones 72).  Else 0.
-uint64_t rows_first(uint64_t rows, uint64_t cols, uint64_t depth) {
+// would begin another round, goes to a launch of its own, which costs 6 us
+// beside its work.  A last round of small tiles that is at most half full costs
+// half of one (2112 tiles 4.2 rounds, 1056 2.5).  Measured in one launch and in
+// two: 4100 x 4096 x 4096 (rows, contraction, columns) 66 and 52 us, 4346 x
+// 2048 x 16384 114 and 107; in one by this rule: 4100 x 1024 x 8190 38 and 44,
+// 506 x 8192 x 57344 152 and 166.  Of 390 products that it sends in two, 363
+// were faster for it (9% on average) and the others up to 10% slower.
+uint64_t rows_first(uint64_t rows, uint64_t cols, uint64_t depth, size_t bytes) {
   const uint64_t main = rows / 256 * 256;
   if (main == 0 || main == rows) return 0;
-  const Tiles all = tiles_for(kDense, rows, cols, depth, 1);
-  const Tiles t = tiles_for(kDense, main, cols, depth, 1);
-  const uint64_t best = all.cost_large < all.cost_small ? all.cost_large : all.cost_small;
-  return t.cost_large + 4 * 1024 + depth * 3 / 2 < best ? main : 0;
+  const Tiles all = tiles_for(kDense, rows, cols, depth, 1, bytes);
+  const Tiles t = tiles_for(kDense, main, cols, depth, 1, bytes);
+  const uint64_t small = ceil_div(all.small, 256) * all.round_small / 2;
+  const uint64_t best = all.cost_large < small ? all.cost_large : small;
+  const uint64_t rest = cost_of_few(rows - main, cols, depth, bytes);
+  return t.cost_large + 6 * 1024 + rest < best ? main : 0;
 }
 
 template <int MODE>
@@ -734,7 +773,7 @@ ec_status ec_mx_product(const void* a_codes, const void* a_scales, uint64_t rows
   ec_status st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, y, type);
   if (st != EC_OK || rows == 0) return st;
   if (depth == 0) return EC_ERR_INVALID;
-  if (const uint64_t first = rows_first(rows, cols, depth)) {
+  if (const uint64_t first = rows_first(rows, cols, depth, type_bytes(type))) {
     st = ec_mx_product((const uint8_t*)a_codes + first * (depth / 2),
                        (const uint8_t*)a_scales + first * (depth / 32), rows - first, b_codes,
                        b_scales, cols, depth, (uint8_t*)y + first * cols * type_bytes(type), type,
@@ -789,6 +828,19 @@ ec_status ec_mx_product_tokens(const void* a_codes, const void* a_scales, uint64
   p.y = y, p.rows = rows, p.cols = (uint32_t)cols, p.depth = (uint32_t)depth;
   p.offsets = offsets, p.experts = experts, p.tokens = tokens;
   return tiles<kTokens>(p, type, (hipStream_t)stream);
+}
+
+uint32_t ec_mx_product_tile(uint64_t rows, uint64_t cols, uint64_t depth, int type,
+                            uint32_t experts, uint64_t tokens) {
+  if (!type_known(type) || rows == 0 || cols == 0 || (tokens && !experts)) return 0;
+  const int mode = tokens ? kTokens : experts ? kExperts : kDense;
+  if (mode == kDense && rows <= kFewRows) return kFewRows;
+  return side_of(tiles_for(mode, rows, cols, mean_depth(mode, depth, tokens, experts), experts,
+                           type_bytes(type)));
+}
+
+uint64_t ec_mx_product_rows_first(uint64_t rows, uint64_t cols, uint64_t depth, int type) {
+  return type_known(type) ? rows_first(rows, cols, depth, type_bytes(type)) : 0;
 }
 
 size_t ec_mx_linear_workspace_bytes(uint64_t rows, uint64_t depth, uint64_t cols,

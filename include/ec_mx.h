@@ -111,6 +111,16 @@ ec_status ec_mx_product_tokens(const void* a_codes, const void* a_scales, uint64
                                uint64_t tokens, const int32_t* offsets, uint32_t experts, void* y,
                                int type, void* stream);
 
+/* What a product of these sizes runs as. ec_mx_product_tile: rows and columns
+ * of a tile (256, 128 or 64; 16 where the kernel for few rows runs) in
+ * ec_mx_product (experts = 0), ec_mx_product_experts, or, with tokens > 0,
+ * ec_mx_product_tokens, where depth is not used; 0 if there is no such
+ * product. ec_mx_product_rows_first: the rows that ec_mx_product puts into a
+ * launch of their own, before one for the rest (0: all go in one). */
+uint32_t ec_mx_product_tile(uint64_t rows, uint64_t cols, uint64_t depth, int type,
+                            uint32_t experts, uint64_t tokens);
+uint64_t ec_mx_product_rows_first(uint64_t rows, uint64_t cols, uint64_t depth, int type);
+
 /* y [rows][cols] = Q(x) w^T: x [rows][depth] is quantized along its rows on
  * the way, w [cols][padded(depth)] is in the 4-bit form.  With experts > 0,
  * rows are grouped by offsets and w is [experts][cols][padded(depth)]; else
