@@ -424,7 +424,8 @@ struct Few {
   void* y;
   const int32_t* offsets;
   uint64_t rows;
-  uint32_t cols, depth, experts, n_tiles;
+  uint32_t cols, depth, n_tiles;
+  uint32_t experts;      // of x unquantized; 0: none
   uint32_t held, shift;  // rows of a workgroup: up to held, of groups 2^shift = held
 };
 
@@ -445,17 +446,18 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void mx_few(const Few p) {
   const uint32_t r = lane & 15, g = lane >> 4;
   const uint32_t block = block_number(), tn = block % p.n_tiles;
   const uint32_t n0 = tn * kFewCols * NT;
-  if (!p.experts && block >= p.n_tiles) return;
+  // (experts' rows come unquantized: in the 4-bit form they go to the tiles)
+  const uint32_t experts = QUANTIZE ? p.experts : 0;
+  if (!experts && block >= p.n_tiles) return;
   uint64_t row0 = 0;
   uint32_t here = (uint32_t)p.rows;
   T* y = (T*)p.y;
   const uint8_t *bc = p.b.codes, *bs = p.b.scales;
-  if (p.experts) {
-    const GroupTile gt =
-        find_tile(p.offsets, p.experts, p.rows, p.shift, block / p.n_tiles);
+  if (experts) {
+    const GroupTile gt = find_tile(p.offsets, experts, p.rows, p.shift, block / p.n_tiles);
     const uint64_t skip = (uint64_t)gt.local << p.shift;
-    if (gt.group == p.experts) {  // rows of no group: zeros
-      const int64_t f = p.offsets[p.experts];
+    if (gt.group == experts) {  // rows of no group: zeros
+      const int64_t f = p.offsets[experts];
       const uint64_t m0 = (f < 0 ? 0 : f) + skip, end = min(m0 + p.held, p.rows);
       const uint32_t col = n0 + threadIdx.x % (kFewCols * NT);
       if (col < p.cols)

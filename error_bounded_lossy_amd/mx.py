@@ -340,7 +340,7 @@ def mx_linear_backward(dy: torch.Tensor, saved: MXLinearSaved, stream=None):
     return mx_product(dr, saved.w, dy.dtype), mx_product(dc, saved.x, dy.dtype)
 
 
-def _quantize_groups(x, offsets, experts, rows_too=True):
+def _quantize_groups(x, offsets, experts):
     r, stride = _rows(x)
     rows, cols = x.shape
     L = _b.lib()
