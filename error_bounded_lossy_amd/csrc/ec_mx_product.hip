@@ -727,10 +727,12 @@ ec_status few(const Few& p, int type, bool quantize, hipStream_t s) {
   }
 }
 
+// The limit of a row's length holds for `row`, depth without what groups add to it (the
+// kernels' offsets within a tile hold up to 2^25 elements).
 ec_status check(const void* a, const void* sa, uint64_t rows, const void* b, const void* sb,
-                uint64_t cols, uint64_t depth, const void* y, int type) {
+                uint64_t cols, uint64_t depth, uint64_t row, const void* y, int type) {
   if (!type_known(type) || cols == 0 || depth % 128 != 0) return EC_ERR_INVALID;
-  if (rows > EC_MX_MAX_ROWS || cols > EC_MX_MAX_ROWS || depth > EC_MX_MAX_DEPTH)
+  if (rows > EC_MX_MAX_ROWS || cols > EC_MX_MAX_ROWS || row > EC_MX_MAX_DEPTH)
     return EC_ERR_UNSUPPORTED;
   if (rows == 0) return EC_OK;
   if (!y || !aligned(y, type_bytes(type))) return EC_ERR_INVALID;
@@ -772,7 +774,7 @@ extern "C" {
 ec_status ec_mx_product(const void* a_codes, const void* a_scales, uint64_t rows,
                         const void* b_codes, const void* b_scales, uint64_t cols, uint64_t depth,
                         void* y, int type, void* stream) {
-  ec_status st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, y, type);
+  ec_status st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, depth, y, type);
   if (st != EC_OK || rows == 0) return st;
   if (depth == 0) return EC_ERR_INVALID;
   if (const uint64_t first = rows_first(rows, cols, depth, type_bytes(type))) {
@@ -803,7 +805,7 @@ ec_status ec_mx_product_experts(const void* a_codes, const void* a_scales, uint6
                                 int type, void* stream) {
   ec_status st = check_groups(offsets, experts);
   if (st != EC_OK) return st;
-  st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, y, type);
+  st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, depth, y, type);
   if (st != EC_OK || rows == 0) return st;
   if (depth == 0) return EC_ERR_INVALID;
   Product p{};
@@ -822,7 +824,8 @@ ec_status ec_mx_product_tokens(const void* a_codes, const void* a_scales, uint64
   if (st != EC_OK) return st;
   if (tokens > EC_MX_MAX_ROWS) return EC_ERR_UNSUPPORTED;
   const uint64_t depth = ec_mx_padded_groups(tokens, experts);
-  st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, y, type);
+  st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, ec_mx_padded(tokens), y,
+             type);
   if (st != EC_OK || rows == 0) return st;
   Product p{};
   p.a = {(const uint8_t*)a_codes, (const uint8_t*)a_scales};

@@ -46,9 +46,10 @@ extern "C" {
 typedef enum { EC_TYPE_F32 = 0, EC_TYPE_F16 = 1, EC_TYPE_BF16 = 2 } ec_type;
 
 #define EC_MX_BLOCK 32u
-/* Longest row (elements, padded), most groups, and most rows of one call.
- * Calls of more than 2^31 - 1 workgroups (a quantization of 64 rows of up to
- * 128 elements is one) are EC_ERR_UNSUPPORTED too. */
+/* Longest row (elements, padded, without what groups add to it), most groups,
+ * and most rows of one call. Calls of more than 2^31 - 1 workgroups (a
+ * quantization of 64 rows of up to 128 elements is one) are
+ * EC_ERR_UNSUPPORTED too. */
 #define EC_MX_MAX_DEPTH (1u << 24)
 #define EC_MX_MAX_GROUPS 1024u
 #define EC_MX_MAX_ROWS 0x7fffff00u

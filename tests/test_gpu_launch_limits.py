@@ -78,3 +78,21 @@ def test_exchange_of_many_narrow_tokens():
     code, s = R.quantize(xs[at])
     assert torch.equal(R.unpack(q.codes[at]), code.int()) and torch.equal(q.scales[at].int(), s.int())
     assert not q.codes[kept:].any() and not q.scales[kept:].any()
+
+
+def test_training_over_the_longest_row_of_tokens():
+    # ones among zeros: every sum is a whole number that fp32 holds
+    rows, depth, cols = 2 ** 24, 8, 8
+    g = torch.Generator("cuda").manual_seed(4)
+    x = (torch.rand(rows, depth, generator=g, device="cuda") < 0.3).bfloat16()
+    dy = (torch.rand(rows, cols, generator=g, device="cuda") < 0.3).bfloat16()
+    w = torch.ones(3, cols, depth, dtype=torch.bfloat16, device="cuda")
+    at = [0, 5_000_001, 5_000_002, rows]
+    offsets = torch.tensor(at, dtype=torch.int32, device="cuda")
+    y, saved = ec.mx_experts_forward(x, w, offsets)
+    dx, dw = ec.mx_experts_backward(dy, saved)
+    assert torch.equal(y.float(), x.float().sum(1, keepdim=True).expand(-1, cols))
+    assert torch.equal(dx.float(), dy.float().sum(1, keepdim=True).expand(-1, depth))
+    for e, (a, b) in enumerate(zip(at, at[1:])):
+        want = (dy[a:b].t().contiguous().double() @ x[a:b].double()).float().bfloat16()
+        assert torch.equal(dw[e], want)

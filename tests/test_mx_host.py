@@ -197,3 +197,13 @@ def test_rows_that_go_first_depend_on_the_columns(L):
     assert first(4100, 8190, 1024, BF16) == 0
     # whole tiles, or none
     assert first(4096, 4096, 4096, BF16) == first(255, 57344, 8192, BF16) == 0
+
+
+def test_tokens_of_the_longest_row_in_groups(L):
+    # what quantization per group takes, the product over the tokens takes too: the missing y is
+    # what these calls are refused for
+    for experts in (1, 16, 1024):
+        assert L.ec_mx_product_tokens(F, F, 8, F, F, 8, 1 << 24, F, experts, None, BF16, None) == INVALID
+        assert L.ec_mx_product_tokens(F, F, 8, F, F, 8, (1 << 24) + 1, F, experts, None, BF16, None) == UNSUPPORTED
+        assert L.ec_mx_quantize_groups(None, BF16, 1 << 24, 8, 8, F, experts, F, F, F, F, None) == INVALID
+        assert L.ec_mx_quantize_groups(None, BF16, (1 << 24) + 1, 8, 8, F, experts, F, F, F, F, None) == UNSUPPORTED
