@@ -30,7 +30,7 @@ def elsewhere(t: torch.Tensor) -> bool:
 
 def capturing(t: torch.Tensor) -> bool:
     """Whether calls on t, on the current stream, are being recorded into a graph."""
-    return t.get_device() >= 0 and torch.cuda.is_current_stream_capturing()
+    return t.get_device() >= 0 and torch._C._cuda_isCurrentStreamCapturing()
 
 
 def _tensors(v):

@@ -111,9 +111,10 @@ def expert_dispatch_mx(x: torch.Tensor, routing: Routing, stream=None) -> MXTens
     x, kind = _tokens(x, r, "expert_dispatch_mx")
     cols = x.shape[1]
     q = _empty((r.tokens * r.choices,), cols, x)
+    at = q.home.data_ptr()
     _b.check(_b.lib().ec_expert_dispatch_mx(x.data_ptr(), kind, r.tokens, cols,
                                             r.place.data_ptr(), r.choices, r.offsets.data_ptr(),
-                                            r.experts, *q.pointers(),
+                                            r.experts, at, at + q._split,
                                             _b.current_stream(x)), "ec_expert_dispatch_mx")
     return q
 

@@ -42,68 +42,66 @@ def _rows(x: torch.Tensor) -> tuple[torch.Tensor, int]:
     return x, x.shape[1]
 
 
-def padded(cols: int) -> int:
-    return (cols + 127) // 128 * 128
-
-
 class MXTensor:
     """A tensor in the 4-bit form along its last dimension, of `cols` elements:
     codes, uint8 [..., padded / 2], and scales, uint8 [..., padded / 32]."""
 
-    # What the library makes holds both in one allocation, `home`, codes first (`_scales` is None),
-    # and has them as tensors only when asked: an allocation or a view costs the host as much as a
-    # small kernel.  Addresses are taken from the tensors at each call: copies, and tensors whose
-    # memory the caller replaces, are read where they are.
-    __slots__ = ("cols", "padded", "lead", "home", "_scales", "_split", "_forms")
+    # What the library makes holds both in one allocation, `home`, codes first (`_scales` is None,
+    # and `_split` the bytes of codes), and has them as tensors only when asked: an allocation or a
+    # view costs the host as much as a small kernel.  Addresses are taken from the tensors at each
+    # call: copies, and tensors whose memory the caller replaces, are read where they are.
+    __slots__ = ("cols", "padded", "lead", "home", "_scales", "_split", "_checked")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
-        p = padded(cols)
+        p = (cols + 127) // 128 * 128
+        *lead, half = form = codes.shape
         if (codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or cols < 0
-                or codes.shape[-1] * 2 != p or scales.shape[-1] * 32 != p
-                or codes.shape[:-1] != scales.shape[:-1]
+                or half * 2 != p or scales.shape != (*lead, p // 32)
                 or not codes.is_contiguous() or not scales.is_contiguous()
                 or codes.device != scales.device):
             _refuse("MXTensor: uint8 codes [..., padded / 2] and scales [..., padded / 32], "
                     "contiguous and on one device, are wanted")
-        self.cols, self.padded, self.lead = cols, p, codes.shape[:-1]
-        self.home, self._scales = codes, scales
-        self._split, self._forms = None, (codes.shape, scales.shape)
+        self.cols, self.padded, self.lead = cols, p, form[:-1]
+        self.home, self._scales, self._split = codes, scales, codes.numel()
+        self._checked = codes.data_ptr(), scales.data_ptr()
 
     def __reduce__(self):
         return _restored, (self.home, self._scales, tuple(self.lead), self.cols, self.padded)
 
-    def _whole(self) -> torch.Tensor:
-        """home, if it still has the size that codes and scales take."""
-        if self.home.numel() != self._split // 16 * 17:
-            _refuse("MXTensor: its memory was replaced by some of another size")
-        return self.home
+    def _moved(self) -> tuple[int, int]:
+        """The addresses of a caller's tensors that are not where or what they were."""
+        for t, per in ((self.home, 2), (self._scales, 32)):
+            if (t.shape != (*self.lead, self.padded // per) or t.dtype != torch.uint8
+                    or not t.is_contiguous() or t.device != self.home.device):
+                _refuse("MXTensor: its memory was replaced by some of another form")
+        self._checked = self.home.data_ptr(), self._scales.data_ptr()
+        return self._checked
 
-    def _given(self, t: torch.Tensor, form: torch.Size) -> int:
-        """Where t is, if it still has the form that the constructor checked."""
-        if (t.shape != form or t.dtype is not torch.uint8 or not t.is_contiguous()
-                or t.get_device() != self.home.get_device()):
-            _refuse("MXTensor: its memory was replaced by some of another form")
-        return t.data_ptr()
+    def pointers(self) -> tuple[int, int]:
+        """Where codes and scales are now."""
+        scales = self._scales
+        if scales is None:
+            start = self.home.data_ptr()
+            return start, start + self._split
+        codes = self.home
+        at = codes.data_ptr(), scales.data_ptr()
+        if (at != self._checked or codes.numel() != self._split
+                or scales.numel() * 16 != self._split or not codes.is_contiguous()
+                or not scales.is_contiguous()):
+            return self._moved()
+        return at
 
     @property
     def codes(self) -> torch.Tensor:
         if self._scales is not None:
             return self.home
-        return self._whole()[:self._split].view(*self.lead, self.padded // 2)
+        return self.home[:self._split].view(*self.lead, self.padded // 2)
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is not None:
             return self._scales
-        return self._whole()[self._split:].view(*self.lead, self.padded // 32)
-
-    def pointers(self) -> tuple[int, int]:
-        """Where codes and scales are now."""
-        if self._scales is None:
-            start = self._whole().data_ptr()
-            return start, start + self._split
-        codes, scales = self._forms
-        return self._given(self.home, codes), self._given(self._scales, scales)
+        return self.home[self._split:].view(*self.lead, self.padded // 32)
 
     @property
     def codes_ptr(self) -> int:
@@ -127,11 +125,11 @@ class MXTensor:
 
 def _empty(lead, cols, like, p=None) -> MXTensor:
     m = object.__new__(MXTensor)
-    m.cols, m.padded, m.lead = cols, padded(cols) if p is None else p, lead
+    m.cols, m.padded, m.lead = cols, (cols + 127) // 128 * 128 if p is None else p, lead
     # bytes of codes, the scales behind: a multiple of 64, so both are aligned
     m._split = math.prod(lead) * (m.padded // 2)
     m.home = like.new_empty(m._split // 16 * 17, dtype=torch.uint8)
-    m._scales = m._forms = None
+    m._scales = m._checked = None
     return m
 
 
@@ -142,11 +140,10 @@ def _restored(home, scales, lead, cols, p) -> MXTensor:
     m = object.__new__(MXTensor)
     m.cols, m.padded, m.lead, m.home = cols, p, torch.Size(lead), home
     m._split = math.prod(lead) * (p // 2)
-    m._scales = m._forms = None
-    if (home.dtype != torch.uint8 or home.dim() != 1 or not home.is_contiguous() or cols < 0
-            or p % 128 or p < cols):
+    m._scales = m._checked = None
+    if (home.dtype != torch.uint8 or home.shape != (m._split // 16 * 17,)
+            or not home.is_contiguous() or cols < 0 or p % 128 or p < cols):
         _refuse("MXTensor: uint8 memory in one piece is wanted, and rows padded to 128 elements")
-    m._whole()
     return m
 
 
@@ -159,8 +156,9 @@ def mx_quantize(x: torch.Tensor, stream=None) -> MXTensor:
         _refuse("mx_quantize: at least one element a row is wanted")
     r, stride = _rows(x)
     q = _empty(x.shape[:-1], x.shape[-1], x)
-    _b.check(_b.lib().ec_mx_quantize(r.data_ptr(), kind, r.shape[0], r.shape[1], stride,
-                                     *q.pointers(), _b.current_stream(x)), "ec_mx_quantize")
+    at = q.home.data_ptr()
+    _b.check(_b.lib().ec_mx_quantize(r.data_ptr(), kind, r.shape[0], r.shape[1], stride, at,
+                                     at + q._split, _b.current_stream(x)), "ec_mx_quantize")
     return q
 
 
@@ -182,10 +180,10 @@ def mx_quantize_both(x: torch.Tensor, stream=None) -> tuple[MXTensor, MXTensor]:
     batch = x.shape[0] if x.dim() == 3 else 1
     a, b = _empty((*lead, rows), cols, x), _empty((*lead, cols), rows, x)
     if rows and batch:
+        at, bt = a.home.data_ptr(), b.home.data_ptr()
         _b.check(_b.lib().ec_mx_quantize_both(
-            x.data_ptr(), kind, batch, rows, cols, batch_stride, stride,
-            *a.pointers(), *b.pointers(),
-            _b.current_stream(x)), "ec_mx_quantize_both")
+            x.data_ptr(), kind, batch, rows, cols, batch_stride, stride, at, at + a._split, bt,
+            bt + b._split, _b.current_stream(x)), "ec_mx_quantize_both")
     return a, b
 
 
@@ -194,7 +192,7 @@ def mx_dequantize(q: MXTensor, dtype: torch.dtype = torch.float32, stream=None) 
     if stream is not None or _b.elsewhere(q.home):
         return _b.on_stream(mx_dequantize, (q, dtype), stream)
     kind = TYPES.get(dtype)
-    if kind is None or not q.home.is_cuda or q.cols == 0 or q.padded != padded(q.cols):
+    if kind is None or not q.home.is_cuda or q.cols == 0 or q.padded - q.cols > 127:
         _refuse("mx_dequantize: a nonempty row on the GPU and float32, float16 or bfloat16 are wanted")
     lead = q.lead
     y = q.home.new_empty((*lead, q.cols), dtype=dtype)
@@ -219,7 +217,7 @@ def mx_product(a: MXTensor, b: MXTensor, dtype: torch.dtype = torch.bfloat16,
         return _b.on_stream(mx_product, (a, b, dtype), stream)
     kind = TYPES.get(dtype)
     if (kind is None or len(a.lead) != 1 or len(b.lead) != 1 or a.cols != b.cols or a.cols == 0
-            or not a.padded == b.padded == padded(a.cols)
+            or a.padded != b.padded or a.padded - a.cols > 127
             or not a.home.is_cuda or a.home.device != b.home.device):
         _refuse("mx_product: [rows, depth] and [cols, depth] on one GPU are wanted")
     rows, cols = a.lead[0], b.lead[0]
@@ -232,7 +230,7 @@ def mx_product(a: MXTensor, b: MXTensor, dtype: torch.dtype = torch.bfloat16,
 def _linear(x, w, offsets, experts, what):
     kind = _type(x, what)
     cols, depth = w.lead[-1], x.shape[-1]
-    if (w.cols != depth or depth == 0 or w.padded != padded(depth)
+    if (w.cols != depth or depth == 0 or w.padded - depth > 127
             or w.home.device != x.device):
         _refuse(f"{what}: weights [.., cols, depth] on the device of x [.., depth] are wanted")
     r, stride = _rows(x)
@@ -278,7 +276,7 @@ def mx_experts_product(a: MXTensor, b: MXTensor, offsets: torch.Tensor,
     if stream is not None or _b.elsewhere(a.home):
         return _b.on_stream(mx_experts_product, (a, b, offsets, dtype), stream)
     if (dtype not in TYPES or len(a.lead) != 1 or len(b.lead) != 2 or a.cols != b.cols
-            or a.cols == 0 or 0 in b.lead or not a.padded == b.padded == padded(a.cols)
+            or a.cols == 0 or 0 in b.lead or a.padded != b.padded or a.padded - a.cols > 127
             or not a.home.is_cuda
             or a.home.device != b.home.device):
         _refuse("mx_experts_product: [rows, depth] and [experts, cols, depth] on one GPU are wanted")
@@ -347,9 +345,10 @@ def _quantize_groups(x, offsets, experts):
     a = _empty((rows,), cols, x)
     b = _empty((cols,), rows, x, int(L.ec_mx_padded_groups(rows, experts)))
     if rows:
+        at, bt = a.home.data_ptr(), b.home.data_ptr()
         _b.check(L.ec_mx_quantize_groups(r.data_ptr(), TYPES[x.dtype], rows, cols, stride,
-                                         offsets.data_ptr(), experts, *a.pointers(),
-                                         *b.pointers(), _b.current_stream(x)),
+                                         offsets.data_ptr(), experts, at, at + a._split, bt,
+                                         bt + b._split, _b.current_stream(x)),
                  "ec_mx_quantize_groups")
     return a, b
 
