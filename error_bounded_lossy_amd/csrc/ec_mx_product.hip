@@ -448,7 +448,6 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void mx_few(const Few p) {
   const uint32_t n0 = tn * kFewCols * NT;
   // (experts' rows come unquantized: in the 4-bit form they go to the tiles)
   const uint32_t experts = QUANTIZE ? p.experts : 0;
-  if (!experts && block >= p.n_tiles) return;
   uint64_t row0 = 0;
   uint32_t here = (uint32_t)p.rows;
   T* y = (T*)p.y;
@@ -471,6 +470,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void mx_few(const Few p) {
     here = (uint32_t)min((uint64_t)p.held, gt.count - skip);
     bc += (uint64_t)gt.group * p.cols * (p.depth / 2);
     bs += (uint64_t)gt.group * p.cols * (p.depth / 32);
+  } else if (block >= p.n_tiles) {
+    return;
   }
   const uint32_t pitch = p.depth / 2, spitch = p.depth / 32;
   const uint32_t steps = p.depth / 128, pieces = (steps + 3) / 4;
