@@ -57,9 +57,10 @@ struct Product {
 // xor bits 1 and 2 of the row, so that 8 lanes of consecutive rows read 8
 // different 16-byte columns of 128.
 //
-// 8192 x 8192 x 8192 in bf16: 300 us (3.7 PFLOP/s), of which the instructions
-// alone take 270 at the clock that random codes leave (202 on zeros); loads and
-// LDS reads alone take 220.
+// 8192 x 8192 x 8192 in bf16: 310 us in a loop of its own (3.5 PFLOP/s; 326 to
+// 341 among other kernels, fp32 362), of which the instructions alone take 270 at
+// the clock that random codes leave (202 on zeros); loads and LDS reads alone
+// take 220.
 //
 // Scales come 16 bytes a row, once in four stages, through registers: 4 bytes
 // a row and stage would be as many requests of the caches as the codes are

@@ -3,7 +3,8 @@ tokens sorted by expert and brought back with weights applied, with the
 gradients of both ways, and a dispatch that sends the 4-bit form of mx.py.
 
 Calls run on torch's current stream of the tensors' device, or on `stream`, on
-which the results are then allocated.
+which the results are then allocated.  Results carry no autograd history: the
+gradients are functions of their own.
 """
 from __future__ import annotations
 

@@ -5,7 +5,9 @@ of a layer and of an expert layer built from them.
 Like the rest of the binding this module only checks and marshals arguments;
 every step runs in the library's kernels on torch's current stream of the
 tensors' device, or on `stream`, on which the results are then allocated (the
-caller orders that stream after what produced the inputs).
+caller orders that stream after what produced the inputs).  Results carry no
+autograd history, whatever their inputs have: gradients come from the backward
+functions, which a torch.autograd.Function may call.
 """
 from __future__ import annotations
 

@@ -6,7 +6,7 @@
  *
  * A token t has `choices` experts ids[t][j].  An id outside [0, experts) (a
  * router writes -1) is a dropped choice: it takes part in nothing, and what
- * its weight holds is not read.
+ * its weight holds has no effect.
  *   - order, i32 [tokens * choices]: row r of the sorted array is the flat
  *     choice order[r] = t * choices + j; choices of one expert keep their
  *     order; rows at offsets[experts] and beyond are -1.
