@@ -165,7 +165,7 @@ struct Shape {
   uint64_t tokens;
   uint32_t cols, chunks, shift, choices;
   uint64_t rows;  // tokens * choices
-  bool past;      // stores go past the caches
+  bool past;      // stores of 16-bit types go past the caches
 };
 
 struct At {
@@ -199,7 +199,8 @@ __device__ __forceinline__ void clear_rows(T* xs, const Shape& s, const At& a, u
       store_eight(xs + r * s.cols + c * 8, (int64_t)s.cols - c * 8, Eight<T>{}, s.past);
 }
 
-// 16384 tokens, 4 choices, 4096 bf16: 109 us (6.2 TB/s).
+// 16384 tokens, 4 choices, 4096 bf16: 110 us in a loop of its own (6.1 TB/s), 133
+// among the other moves, whose lines the caches still write back.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void expert_dispatch(const T* __restrict__ x, Shape s,
                                                             const int32_t* __restrict__ place,
@@ -247,8 +248,9 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch_mx(
 // y[t] = sum over the choices of w (or 1) times the choice's row, in fp32 and
 // in the choices' order.  A lane has PIECES pieces of J rows in flight, and
 // places and weights are looked up once for all of them.  16384 tokens, 4
-// choices, 4096 bf16: 139-145 us with weights, 124 without (4.7 and 5.4 TB/s);
-// with one piece 151 and 131.
+// choices, 4096 bf16: 108 us with weights after a dispatch, 125 without after a
+// combine's gradient (6.2 and 5.4 TB/s), 119 and 126 in loops of their own.  With
+// one piece instead, both took 6 to 8% longer.
 template <typename T, bool WEIGHTED, int PIECES>
 __global__ __launch_bounds__(kThreads) void expert_gather(const T* __restrict__ ys, Shape s,
                                                           const int32_t* __restrict__ place,
@@ -355,7 +357,7 @@ __global__ __launch_bounds__(kThreads) void expert_combine_back(
           dot += p;
           if (here && c < s.chunks)
             store_eight(dys + r * s.cols + (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8,
-                        narrow<T>(g), s.past);
+                        narrow<T>(g));
         }
       }
     // the token's lanes together: within a wave by exchange, else over LDS
@@ -380,10 +382,10 @@ ec_status launched() { return hipGetLastError() == hipSuccess ? EC_OK : EC_ERR_D
 
 // `pieces`: how many a lane should have before the row takes more lanes
 Shape shape_of(uint64_t tokens, uint64_t cols, uint32_t choices, uint32_t chunks,
-               uint32_t pieces, uint64_t bytes_out) {
+               uint32_t pieces, bool past) {
   Shape s{};
   s.tokens = tokens, s.cols = (uint32_t)cols, s.choices = choices, s.rows = tokens * choices;
-  s.chunks = chunks, s.past = past_caches(bytes_out);
+  s.chunks = chunks, s.past = past;
   s.shift = 4;
   while (s.shift < 8 && (pieces << s.shift) < chunks) s.shift++;
   return s;
@@ -461,8 +463,9 @@ ec_status ec_expert_dispatch(const void* x, int type, uint64_t tokens, uint64_t 
   if (!fine(x, type_bytes(type)) || !fine(xs, type_bytes(type)) || !fine(place, 4) ||
       !fine(offsets, 4))
     return EC_ERR_INVALID;
+  const uint64_t row = cols * type_bytes(type);
   const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
-                           tokens * choices * cols * type_bytes(type));
+                           past_caches(tokens * choices * row, row));
   BY_TYPE(type, hipLaunchKernelGGL((expert_dispatch<T>), grid_of(blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)x, s, place,
                                    offsets, experts, (T*)xs));
@@ -479,7 +482,7 @@ ec_status ec_expert_dispatch_mx(const void* x, int type, uint64_t tokens, uint64
       !fine(offsets, 4))
     return EC_ERR_INVALID;
   const Shape s = shape_of(tokens, cols, choices, (uint32_t)(ec_mx_padded(cols) / 8), 2,
-                           0);
+                           false);
   BY_TYPE(type, hipLaunchKernelGGL((expert_dispatch_mx<T>), grid_of(blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)x, s, place,
                                    offsets, experts, (uint8_t*)codes, (uint8_t*)scales));
@@ -493,8 +496,9 @@ ec_status ec_expert_dispatch_backward(const void* dxs, int type, uint64_t tokens
   if (st != EC_OK || tokens == 0) return st;
   if (!fine(dxs, type_bytes(type)) || !fine(dx, type_bytes(type)) || !fine(place, 4))
     return EC_ERR_INVALID;
+  const uint64_t row = cols * type_bytes(type);
   const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
-                           tokens * cols * type_bytes(type));
+                           past_caches(tokens * row, row));
   BY_TYPE(type, hipLaunchKernelGGL((expert_gather<T, false, 2>), grid_of(blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)dxs, s, place,
                                    (const void*)nullptr, 0, (T*)dx));
@@ -511,8 +515,9 @@ ec_status ec_expert_combine(const void* ys, int type, uint64_t tokens, uint64_t 
   if (!fine(ys, type_bytes(type)) || !fine(y, type_bytes(type)) || !fine(place, 4) ||
       !fine(weights, type_bytes(wtype)))
     return EC_ERR_INVALID;
+  const uint64_t row = cols * type_bytes(type);
   const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
-                           tokens * cols * type_bytes(type));
+                           past_caches(tokens * row, row));
   BY_TYPE(type, hipLaunchKernelGGL((expert_gather<T, true, 2>), grid_of(blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)ys, s, place,
                                    weights, wtype, (T*)y));
@@ -532,8 +537,8 @@ ec_status ec_expert_combine_backward(const void* dy, const void* ys, int type, u
   if (!fine(dy, b) || !fine(ys, b) || !fine(dys, b) || !fine(place, 4) || !fine(offsets, 4) ||
       !fine(weights, wb) || !fine(dweights, wb))
     return EC_ERR_INVALID;
-  const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2,
-                           tokens * choices * cols * b);
+  // (stored past the caches dys of 256 MiB to 2 GiB took 2 to 4% longer)
+  const Shape s = shape_of(tokens, cols, choices, (uint32_t)ceil_div(cols, 8), 2, false);
   BY_TYPE(type, hipLaunchKernelGGL((expert_combine_back<T, 2>), grid_of(blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)dy,
                                    (const T*)ys, s, place, weights, wtype, offsets, experts,

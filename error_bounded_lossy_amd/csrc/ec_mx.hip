@@ -84,8 +84,8 @@ __global__ __launch_bounds__(kThreads, 2) void mx_both(
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t cg = lane & 15, rb = lane >> 4;
   const uint32_t pairs = (col_tiles + 1) / 2;
-  const uint32_t block = block_number(), ct = 2 * (block % pairs) + (wave >> 1);
-  const uint64_t rt = 2 * (uint64_t)(block / pairs) + (wave & 1);
+  const uint32_t ct = 2 * (blockIdx.x % pairs) + (wave >> 1);
+  const uint64_t rt = 2 * (uint64_t)(blockIdx.x / pairs) + (wave & 1);
   if (ct >= col_tiles || rt >= row_tiles) return;
   uint64_t first = rt * 128, last = rows;  // this wave's rows
   if (offsets) {
@@ -293,8 +293,7 @@ __global__ __launch_bounds__(kThreads) void mx_values(const uint8_t* __restrict_
     }
     T* to = y + row * stride + c0;
     if (c0 + E <= cols) {
-      if (past) store16_past(to, v);
-      else __builtin_memcpy(to, v, 16);
+      store16(to, v, past);
     } else {
       T e[E];
       __builtin_memcpy(e, v, 16);
@@ -353,8 +352,9 @@ ec_status both_of(const void* x, uint64_t batch, uint64_t rows, uint64_t cols,
   const uint32_t ct = (uint32_t)ceil_div(rc ? pc : cols, width);
   const uint64_t rt = pr / 128;
   const uint64_t blocks = ceil_div(ct, 2) * ceil_div(rt, 2);
-  if (blocks > kMostBlocks) return EC_ERR_UNSUPPORTED;
-  const dim3 grid = grid_of(blocks, (uint32_t)batch), block(kThreads);
+  // (an array of 2^24 - 1 workgroups would have 2^40 elements)
+  if (blocks * kThreads >> 32) return EC_ERR_UNSUPPORTED;
+  const dim3 grid((uint32_t)blocks, 1, (uint32_t)batch), block(kThreads);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, block, 0, s, (const T*)x, rows, (uint32_t)cols, batch_stride,
                        stride, offsets, groups, ct, rt, (uint8_t*)rc, (uint8_t*)rs, (uint8_t*)cc,
@@ -375,7 +375,12 @@ ec_status values_of(const void* codes, const void* scales, uint64_t rows, uint64
   const uint32_t per = many(rows * (padded / E)) ? 4 : 1;
   const uint64_t blocks = tiles * ceil_div(rows, ty * per);
   if (blocks > kMostBlocks) return EC_ERR_UNSUPPORTED;
-  const bool past = past_caches(rows * cols * sizeof(T));
+  // Past the caches from 32 MiB on, what the L2 caches hold, where the pieces of
+  // 16 bytes are aligned: 212992 x 128 fp32 (104 MiB), quantized and back, 41 us,
+  // stored as usual 48; a kernel behind that reads 8192 x 4096 fp32 is done after
+  // 57 with it and 51, of 16384 x 4096 (256 MiB) after 108 and 129. Rows of 989
+  // and of 6498 fp32 took 42 and 56 so, and take 31 and 41.
+  const bool past = stride * sizeof(T) % 16 == 0 && rows * cols * sizeof(T) > (32ull << 20);
   if (per == 4)
     hipLaunchKernelGGL((mx_values<T, 4>), grid_of(blocks), dim3(kThreads), 0, s,
                        (const uint8_t*)codes, (const uint8_t*)scales, rows, (uint32_t)cols, padded,

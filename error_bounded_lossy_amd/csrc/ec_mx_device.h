@@ -37,10 +37,10 @@ inline uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 // more than there is work for: kernels check their numbers anyhow.
 constexpr uint32_t kGridBits = 22;
 constexpr uint64_t kMostBlocks = 0x7fffffffull;
-inline dim3 grid_of(uint64_t blocks, uint32_t z = 1) {
+inline dim3 grid_of(uint64_t blocks) {
   const uint64_t wide = 1ull << kGridBits;
-  return blocks <= wide ? dim3((uint32_t)blocks, 1, z)
-                        : dim3((uint32_t)wide, (uint32_t)ceil_div(blocks, wide), z);
+  return blocks <= wide ? dim3((uint32_t)blocks)
+                        : dim3((uint32_t)wide, (uint32_t)ceil_div(blocks, wide));
 }
 __device__ __forceinline__ uint32_t block_number() {
   return blockIdx.y << kGridBits | blockIdx.x;
@@ -77,29 +77,51 @@ __device__ __forceinline__ Eight<T> load_eight(const T* p, int64_t n) {
   return v;
 }
 
-// Outputs that the 8 L2 caches of 4 MiB cannot hold are stored past them
-// (`past`): lines that wait there only to be written back cost the reads.
-inline bool past_caches(uint64_t bytes) { return bytes > (32ull << 20); }
+// Outputs that the caches cannot keep for who reads them are stored past them
+// (`past`): lines that wait there only to be written back cost the reads. That
+// is from the size of the last-level cache, 256 MiB, on, in rows of whole lines
+// of 128 bytes. Measured with a kernel behind that reads the output, stored as
+// usual and past: products 16384 x 512 x 16384 in bf16 (512 MiB) 363 and 340 us,
+// of half the columns 171 and 173, 8192 x 512 x 8192 83 and 97; rows dispatched,
+// 256 MiB of bf16, 160 and 146, 128 MiB 61 and 69. Where lines are in parts:
+// 16384 x 512 x 8200 170 and 203, dispatched rows of 250 94 and 102.
+inline bool past_caches(uint64_t bytes, uint64_t row_bytes) {
+  return row_bytes % 128 == 0 && bytes >= 256ull << 20;
+}
 
 // 16 bytes to an address with the alignment of an element.
-template <typename T>
-__device__ __forceinline__ void store16_past(T* p, const void* v) {
+template <bool PAST, typename T>
+__device__ __forceinline__ void store16(T* p, const void* v) {
   typedef int unaligned __attribute__((ext_vector_type(4), aligned(2)));
   unaligned w;
   __builtin_memcpy(&w, v, 16);
-  __builtin_nontemporal_store(w, (unaligned*)p);
+  if (PAST) __builtin_nontemporal_store(w, (unaligned*)p);
+  else *(unaligned*)p = w;
+}
+// The same by a branch. The empty statements keep each store as it is: where two
+// branches store alike, the compiler would make one store of both, without the
+// hint, and of a whole piece and of a ragged one the shared last elements. (They
+// also keep other memory operations on their side of the store.)
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const void* v, bool past) {
+  if (past) {
+    asm volatile("");
+    store16<true>(p, v);
+    asm volatile("");
+  } else {
+    store16<false>(p, v);
+    asm volatile("");
+  }
 }
 
 template <typename T>
 __device__ __forceinline__ void store_eight(T* p, int64_t n, const Eight<T>& v,
                                             bool past = false) {
   if (n >= 8) {
-    // (two stores of a lane's 32 bytes leave gaps that only the caches close)
-    if (sizeof(T) == 2 && past) {
-      store16_past(p, v.w);
-    } else {
-      __builtin_memcpy(p, &v, sizeof(v));
-    }
+    // (two stores of a lane's 32 bytes leave gaps that only the caches close: a
+    // dispatch of 16384 x 4 x 4096 fp32 takes 311 us, past them 479)
+    store16(p, v.w, sizeof(T) == 2 && past);
+    if constexpr (sizeof(T) == 4) store16(p + 4, v.w + 4, false);
   } else {
     T e[8];
     __builtin_memcpy(e, &v, sizeof(v));

@@ -33,7 +33,6 @@ struct Product {
   uint32_t experts;
   uint32_t m_tiles, n_tiles;
   uint64_t tokens;   // kTokens: rows that the groups divide
-  bool past;         // stores go past the caches
 };
 
 // ---------------------------------------------------------------- tiles
@@ -151,7 +150,9 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("" ::: "memory");
 }
 
-template <int FM, int FN, typename T, int MODE>
+// PAST: results are stored past the caches (a branch at each store costs 1 us of
+// 45 for 4096 x 4096 x 4096).
+template <int FM, int FN, typename T, int MODE, bool PAST>
 __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx_tiles(const Product p) {
   constexpr int BM = 64 * FM, BN = 64 * FN, kWaves = 4;
   using St = Stage<BM, BN>;
@@ -379,8 +380,7 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx_tiles(const Produ
       if (m < m_end) {
         T* to = y + m * p.cols + nw + col;
         if (nw + col + kE <= p.cols) {
-          if (p.past) store16_past(to, v);
-          else __builtin_memcpy(to, v, 16);
+          store16<PAST>(to, v);
         } else {
 #pragma unroll
           for (uint32_t u = 0; u < kE; u++)
@@ -583,9 +583,22 @@ ec_status tiles_as(Product p, hipStream_t s) {
   const uint64_t tiles = ceil_div(m * p.n_tiles, 8) * 8 * (MODE == kTokens ? p.experts : 1);
   if (tiles > kMostBlocks) return EC_ERR_UNSUPPORTED;
   p.m_tiles = (uint32_t)m;
-  p.past = past_caches(p.rows * p.cols * sizeof(T) * (MODE == kTokens ? p.experts : 1));
-  hipLaunchKernelGGL((mx_tiles<FM, FN, T, MODE>), grid_of(tiles),
-                     dim3(256), 0, s, p);
+  // Weights' gradients are read after the whole backward pass, when no cache has
+  // them: past what the L2 caches hold, 32 MiB, in whole lines (16 x 2048 x 2048
+  // fp32 stored as usual 115 us, past 101; 64 x 4096 x 2048 bf16 575 and 435; not
+  // in rows of 1304 bf16 58 and 70, of 366 fp32 52 and 87). Ragged rows of other
+  // products fill most of their lines as large tiles: from 512 MiB on (32768 x 512
+  // x 16389 bf16 491 and 393; as tiles of 128, 6013 x 384 x 52412, 238 and 346).
+  const uint64_t bytes = p.rows * p.cols * sizeof(T) * (MODE == kTokens ? p.experts : 1);
+  const uint64_t row = p.cols * sizeof(T);
+  if constexpr (FM > 1) {  // under 128 tiles of 128, where those of 64 run, is 8 MiB at most
+    if (MODE == kTokens ? row % 128 == 0 && bytes > (32ull << 20)
+                        : past_caches(bytes, row) || (FM == 4 && bytes >= (512ull << 20))) {
+      hipLaunchKernelGGL((mx_tiles<FM, FN, T, MODE, true>), grid_of(tiles), dim3(256), 0, s, p);
+      return launched();
+    }
+  }
+  hipLaunchKernelGGL((mx_tiles<FM, FN, T, MODE, false>), grid_of(tiles), dim3(256), 0, s, p);
   return launched();
 }
 
