@@ -250,7 +250,7 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch_mx(
 // places and weights are looked up once for all of them.  16384 tokens, 4
 // choices, 4096 bf16: 108 us with weights after a dispatch, 125 without after a
 // combine's gradient (6.2 and 5.4 TB/s), 119 and 126 in loops of their own.  With
-// one piece instead, both took 6 to 8% longer.
+// one piece instead, both took 6% longer.
 template <typename T, bool WEIGHTED, int PIECES>
 __global__ __launch_bounds__(kThreads) void expert_gather(const T* __restrict__ ys, Shape s,
                                                           const int32_t* __restrict__ place,

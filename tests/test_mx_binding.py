@@ -203,3 +203,65 @@ def test_inputs_stay_for_another_stream_also_when_a_call_fails(monkeypatch, fail
     with (pytest.raises(ec.ECError) if fails else contextlib.nullcontext()):
         _binding.on_stream(call, (x,), s)
     assert recorded == [s]
+
+
+# ---------------------------------------------------------------- every call, on a stream of its own
+
+
+def every_call():
+    r = ec.expert_sort(gpu(torch.zeros(6, 2, dtype=torch.int32)), 4)
+    offsets = gpu(torch.tensor([0, 3, 6], dtype=torch.int32))
+    x, w, we = gpu(torch.zeros(6, 64)), gpu(torch.zeros(32, 64)), gpu(torch.zeros(2, 32, 64))
+    rows, wt = gpu(torch.zeros(12, 64)), gpu(torch.zeros(6, 2))
+    dy = gpu(torch.zeros(6, 32))
+    linear, experts = ec.mx_linear_forward(x, w)[1], ec.mx_experts_forward(x, we, offsets)[1]
+    return {
+        "mx_quantize": (x,), "mx_quantize_both": (x,), "mx_dequantize": (form(6, 64), torch.float16),
+        "mx_product": (form(6, 64), form(32, 64), torch.float16), "mx_linear": (x, form(32, 64)),
+        "mx_experts_linear": (x, form(2, 32, 64), offsets),
+        "mx_experts_product": (form(6, 64), form(2, 32, 64), offsets, torch.float16),
+        "mx_linear_forward": (x, w), "mx_linear_backward": (dy, linear),
+        "mx_experts_forward": (x, we, offsets), "mx_experts_backward": (dy, experts),
+        "expert_sort": (gpu(torch.zeros(6, 2, dtype=torch.int32)), 4), "expert_dispatch": (x, r),
+        "expert_dispatch_mx": (x, r), "expert_dispatch_backward": (rows, r), "expert_combine": (rows, r, wt),
+        "expert_combine_backward": (x, rows, r, wt),
+    }
+
+
+# A call on a stream, and one on tensors of a GPU that is not the current one, go through the same
+# function again under that stream and device: with the same arguments in the same places.
+@pytest.mark.parametrize("elsewhere", [False, True])
+def test_calls_elsewhere_make_the_same_library_calls(monkeypatch, stub, elsewhere):
+    import contextlib
+
+    class Stream:
+        device, stream_id = torch.device("cpu"), 1
+
+    seen = []
+    monkeypatch.setattr(Stub, "__getattr__", lambda self, name: (
+        getattr(self.real, name) if name.endswith("_bytes") or "padded" in name else
+        lambda *args: (seen.append((name, args)), ec.EC_OK)[1]))
+    stub()
+    for name in ("device", "stream"):
+        monkeypatch.setattr(torch.cuda, name, lambda *a: contextlib.nullcontext())
+    recorded = []
+    monkeypatch.setattr(OnGPU, "record_stream", lambda self, s: recorded.append(self.data_ptr()), raising=False)
+    public = {n for names in ec._OPERATORS.values() for n in names if n[0].islower()}
+    calls = every_call()
+    assert set(calls) == public
+    inputs = lambda args: [v for v in args if isinstance(v, int) and 0 <= v < 1 << 32]  # noqa: E731 (no addresses)
+    for name, args in calls.items():
+        seen.clear()
+        getattr(ec, name)(*args)
+        plain = [(n, inputs(a)) for n, a in seen]
+        seen.clear()
+        recorded.clear()
+        away = [True]
+        if elsewhere:  # once: the call under the device is not elsewhere any more
+            monkeypatch.setattr(_binding, "elsewhere", lambda t: away.pop() if away else False)
+            getattr(ec, name)(*args)
+            assert not away and not recorded
+        else:
+            getattr(ec, name)(*args, stream=Stream())
+            assert {t.data_ptr() for a in args for t in _binding._tensors(a)} == set(recorded)
+        assert [(n, inputs(a)) for n, a in seen] == plain and plain, name
