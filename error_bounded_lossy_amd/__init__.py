@@ -15,7 +15,8 @@ import re
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB_PATH = os.path.join(HERE, "libec.so")
-HEADERS = [os.path.join(ROOT, "include", h) for h in ("ec.h", "ec_huffman.h", "ec_mx.h", "ec_experts.h")]
+HEADERS = [os.path.join(ROOT, "include", h) for h in ("ec.h", "ec_huffman.h", "ec_mx.h", "ec_i8.h",
+                                                     "ec_norm.h", "ec_experts.h")]
 
 EC_OK, EC_ERR_INVALID, EC_ERR_CAPACITY, EC_ERR_CORRUPT = 0, 1, 2, 3
 EC_ERR_DEVICE, EC_ERR_OOM, EC_ERR_UNSUPPORTED = 4, 5, 6
@@ -122,7 +123,7 @@ def lib():
     L.ec_huff_encode_segments.argtypes = [vp, ctypes.c_uint32, u64, vp, vp, vp, u64, vp, sz, vp]
     L.ec_huff_decode_segments.restype = st
     L.ec_huff_decode_segments.argtypes = [vp, vp, vp, u64, ctypes.c_uint32, u64, vp, vp, sz, vp]
-    u32, i = ctypes.c_uint32, ctypes.c_int
+    u32, i, f32 = ctypes.c_uint32, ctypes.c_int, ctypes.c_float
     for name, result, args in (
         ("ec_mx_padded", u64, (u64,)),
         ("ec_mx_padded_groups", u64, (u64, u32)),
@@ -137,6 +138,23 @@ def lib():
         ("ec_mx_product_rows_first", u64, (u64, u64, u64, i)),
         ("ec_mx_linear_workspace_bytes", sz, (u64, u64, u64, u32)),
         ("ec_mx_linear", st, (vp, i, u64, u64, u64, vp, vp, u64, vp, u32, vp, vp, sz, vp)),
+        ("ec_i8_quantize", st, (vp, i, u64, u64, u64, vp, vp, vp)),
+        ("ec_i8_dequantize", st, (vp, vp, u64, u64, vp, i, u64, vp)),
+        ("ec_i8_product", st, (vp, vp, u64, vp, vp, u64, u64, vp, i, vp)),
+        ("ec_i8_product_experts", st, (vp, vp, u64, vp, vp, u64, u64, vp, u32, vp, i, vp)),
+        ("ec_i8_product_tile", u32, (u64, u64, u64, i, u32)),
+        ("ec_i8_linear_workspace_bytes", sz, (u64, u64, u64, u32)),
+        ("ec_i8_linear", st, (vp, i, u64, u64, u64, vp, vp, u64, vp, u32, vp, vp, sz, vp)),
+        ("ec_rms_norm", st, (vp, u64, vp, u64, i, u64, u64, vp, i, f32, vp, vp, vp, vp)),
+        ("ec_rms_norm_i8", st, (vp, u64, vp, u64, i, u64, u64, vp, i, f32, vp, vp, vp, vp)),
+        ("ec_rms_norm_backward_workspace_bytes", sz, (u64, u64)),
+        ("ec_rms_norm_backward", st,
+         (vp, vp, vp, i, u64, u64, vp, vp, i, vp, vp, vp, sz, vp)),
+        ("ec_expert_route", st,
+         (vp, i, u64, u64, u32, vp, u32, i, u32, u32, i, f32, vp, vp, vp)),
+        ("ec_expert_route_backward", st,
+         (vp, vp, i, u64, u64, u32, vp, u32, i, i, f32, vp, vp)),
+        ("ec_expert_dispatch_i8", st, (vp, vp, u64, u64, vp, u32, vp, u32, vp, vp, vp)),
         ("ec_expert_sort_workspace_bytes", sz, (u64, u32)),
         ("ec_expert_sort", st, (vp, u32, u64, u32, vp, vp, vp, vp, sz, vp)),
         ("ec_expert_dispatch", st, (vp, i, u64, u64, vp, u32, vp, u32, vp, vp)),
@@ -159,7 +177,7 @@ def declared_functions() -> list[str]:
         with open(h) as f:
             text = f.read()
         text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-        names |= set(re.findall(r"\b(ec_[a-z_]+)\s*\(", text))
+        names |= set(re.findall(r"\b(ec_[a-z0-9_]+)\s*\(", text))
     return sorted(names)
 
 
@@ -533,12 +551,20 @@ _OPERATORS = {
     "experts": ("Routing", "expert_sort", "expert_dispatch", "expert_dispatch_mx",
                 "expert_dispatch_backward", "expert_combine", "expert_combine_backward"),
 }
+# --- what stands around them (include/ec_norm.h, ec_i8.h, ec_experts.h): the norm before a layer,
+# --- the router, and the 8-bit form
+_LAYER_OPERATORS = {
+    "norm": ("RMSNormSaved", "rms_norm", "rms_norm_i8", "rms_norm_forward", "rms_norm_backward"),
+    "i8": ("I8Tensor", "i8_quantize", "i8_dequantize", "i8_product", "i8_linear",
+           "i8_experts_product", "i8_experts_linear"),
+    "experts": ("expert_route", "expert_route_backward", "expert_dispatch_i8"),
+}
 
 
 def __getattr__(name):
     # these modules import torch, which the rest of the binding leaves to its calls
     import importlib
-    for module, names in _OPERATORS.items():
+    for module, names in (*_OPERATORS.items(), *_LAYER_OPERATORS.items()):
         if name in names:
             value = getattr(importlib.import_module(f"{__name__}.{module}"), name)
             globals()[name] = value

@@ -1,4 +1,4 @@
-"""What mx.py and experts.py share: the library, and the stream a call runs on."""
+"""What mx.py, i8.py, norm.py and experts.py share: the library, and the stream a call runs on."""
 from __future__ import annotations
 
 import torch

@@ -245,6 +245,31 @@ __global__ __launch_bounds__(kThreads) void expert_dispatch_mx(
     }
 }
 
+// Rows that are in the 8-bit form, 16 codes a piece.
+__global__ __launch_bounds__(kThreads) void expert_dispatch_i8(
+    const uint4* __restrict__ x, const float* __restrict__ x_scales, Shape s,
+    const int32_t* __restrict__ place, const int32_t* __restrict__ offsets, uint32_t experts,
+    uint4* codes, float* scales) {
+  const At a = at(s);
+  if (a.token >= s.tokens) return;
+  for (uint32_t c = a.lane; c < s.chunks; c += a.lanes) {
+    const uint4 v = x[a.token * s.chunks + c];
+    for (uint32_t j = 0; j < s.choices; j++) {
+      const int64_t r = row_of(place, s, a.token, j);
+      if (r >= 0) codes[r * s.chunks + c] = v;
+    }
+  }
+  for (uint32_t j = a.lane; j < s.choices; j += a.lanes) {
+    const int64_t r = row_of(place, s, a.token, j);
+    if (r >= 0) scales[r] = x_scales[a.token];
+  }
+  for (uint64_t r = no_rows(offsets, experts, s.rows) + a.token; r < s.rows; r += s.tokens) {
+    for (uint32_t c = a.lane; c < s.chunks; c += a.lanes)
+      codes[r * s.chunks + c] = make_uint4(0, 0, 0, 0);
+    if (a.lane == 0) scales[r] = 0;
+  }
+}
+
 // y[t] = sum over the choices of w (or 1) times the choice's row, in fp32 and
 // in the choices' order.  A lane has PIECES pieces of J rows in flight, and
 // places and weights are looked up once for all of them.  16384 tokens, 4
@@ -486,6 +511,24 @@ ec_status ec_expert_dispatch_mx(const void* x, int type, uint64_t tokens, uint64
   BY_TYPE(type, hipLaunchKernelGGL((expert_dispatch_mx<T>), grid_of(blocks_of(s)),
                                    dim3(kThreads), 0, (hipStream_t)stream, (const T*)x, s, place,
                                    offsets, experts, (uint8_t*)codes, (uint8_t*)scales));
+  return launched();
+}
+
+ec_status ec_expert_dispatch_i8(const void* x_codes, const void* x_scales, uint64_t tokens,
+                                uint64_t padded, const int32_t* place, uint32_t choices,
+                                const int32_t* offsets, uint32_t experts, void* codes,
+                                void* scales, void* stream) {
+  ec_status st = check(EC_TYPE_F32, tokens, padded, choices);
+  if (st == EC_OK) st = check_experts(experts);
+  if (st == EC_OK && padded % 128) st = EC_ERR_INVALID;
+  if (st != EC_OK || tokens == 0) return st;
+  if (!read_ok(x_codes, x_scales) || !read_ok(codes, scales) || !fine(place, 4) ||
+      !fine(offsets, 4))
+    return EC_ERR_INVALID;
+  const Shape s = shape_of(tokens, padded, choices, (uint32_t)(padded / 16), 2, false);
+  hipLaunchKernelGGL(expert_dispatch_i8, grid_of(blocks_of(s)), dim3(kThreads), 0,
+                     (hipStream_t)stream, (const uint4*)x_codes, (const float*)x_scales, s, place,
+                     offsets, experts, (uint4*)codes, (float*)scales);
   return launched();
 }
 

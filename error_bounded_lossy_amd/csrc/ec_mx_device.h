@@ -149,6 +149,14 @@ __device__ __forceinline__ Eight<T> narrow(const float (&f)[8]) {
   return v;
 }
 
+// A product that is rounded to fp32 and then to T: for fp16 the compiler would
+// make one instruction of both, which rounds once.
+template <typename T>
+__device__ __forceinline__ float in_fp32(float f) {
+  if constexpr (__is_same(T, f16_t)) asm("" : "+v"(f));
+  return f;
+}
+
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return bits_as<uint32_t>(__builtin_elementwise_max(bits_as<u16x2>(a), bits_as<u16x2>(b)));
 }

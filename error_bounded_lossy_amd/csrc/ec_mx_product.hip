@@ -3,13 +3,12 @@
 // along the contraction, blocks of 32 sharing a scale.
 #include <type_traits>
 
-#include "ec_mx_device.h"
+#include "ec_tile_device.h"
 
 using namespace ecmx;
 
 namespace {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -70,16 +69,6 @@ struct Stage {
   uint8_t b[BN * 64];
 };
 
-// 16 bytes a lane from base + lane_off + off straight to LDS, 1 KiB from `to` on.
-__device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t base, uint32_t lane_off,
-                                         uint32_t off, uint8_t* to) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (__attribute__((address_space(3))) void*)to, 16,
-                                           lane_off, off, 0, 0);
-}
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const uint8_t* p) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0xffffffffu, 0x00027000);
-}
-
 __device__ __forceinline__ i32x8 widened(const i32x4& v) {
   return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};  // 4-bit operands use half
 }
@@ -137,17 +126,6 @@ __device__ __forceinline__ void multiply(const Fragments<FM, FN>& f, const Scale
     between(i);
   }
   __builtin_amdgcn_sched_barrier(0);
-}
-
-// Waits until at most N of this wave's loads are under way and its LDS reads
-// have returned, then for the other waves.
-template <int N>
-__device__ __forceinline__ void wait_and_meet() {
-  static_assert(N < 64, "the counter's range");
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
 }
 
 // PAST: results are stored past the caches (a branch at each store costs 1 us of

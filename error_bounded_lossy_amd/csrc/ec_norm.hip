@@ -1,0 +1,395 @@
+// The root-mean-square norm with the residual's addition (include/ec_norm.h),
+// its output in x's type or in the 8-bit form, and its gradients.  All of it is
+// bound by memory.
+#include <cmath>
+
+#include "ec_norm.h"
+#include "ec_row_device.h"
+
+using namespace ecmx;
+
+namespace {
+
+// Eight weights from element c on; those past the row's end are not used.
+__device__ __forceinline__ void weights_at(const void* w, int type, uint64_t c, int64_t n,
+                                           float (&f)[8]) {
+  if (type == EC_TYPE_F32) widen(load_eight((const float*)w + c, n), f);
+  else if (type == EC_TYPE_F16) widen(load_eight((const f16_t*)w + c, n), f);
+  else widen(load_eight((const bf16_t*)w + c, n), f);
+}
+
+struct Norm {
+  const void *x, *residual, *weight;
+  uint64_t stride, residual_stride;
+  int wtype;
+  float eps;
+  void *h, *y;      // y: rows of x's type, or codes
+  float* scales;    // of codes
+  float* rstd;
+};
+
+// One pass over x and the residual: the row stays in registers (up to 16384
+// elements; longer rows are read again from h, or x, in each pass).
+template <typename T, int PIECES, bool EIGHT_BITS>
+__global__ __launch_bounds__(kRowThreads) void rms_norm(const Norm p, RowShape s) {
+  __shared__ float sums[kRowWaves];
+  __shared__ uint32_t tops[kRowWaves];
+  const RowAt a = row_at(s, block_number());
+  const bool here = a.row < s.rows;
+  const uint64_t row = here ? a.row : s.rows - 1;
+  const T* x = (const T*)p.x + row * p.stride;
+  const T* residual = p.residual ? (const T*)p.residual + row * p.residual_stride : nullptr;
+  T* h = p.h ? (T*)p.h + row * s.cols : nullptr;
+  Eight<T> v[PIECES];
+  float sum = 0;
+  for (uint32_t round = 0; round < s.rounds; round++) {
+#pragma unroll
+    for (int i = 0; i < PIECES; i++) {
+      const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
+      v[i] = load_eight(x + (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8);
+    }
+    if (residual) {
+      Eight<T> r[PIECES];
+#pragma unroll
+      for (int i = 0; i < PIECES; i++) {
+        const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
+        r[i] = load_eight(residual + (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < PIECES; i++) {
+        const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
+        float f[8], g[8];
+        widen(v[i], f);
+        widen(r[i], g);
+#pragma unroll
+        for (int j = 0; j < 8; j++) f[j] += g[j];
+        v[i] = narrow<T>(f);
+        if (here) store_eight(h + (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8, v[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < PIECES; i++) {
+      float f[8];
+      widen(v[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; j++) sum += f[j] * f[j];
+    }
+  }
+  sum = sum_over_row(sum, s.shift, sums);
+  const float rstd = 1.0f / __builtin_sqrtf(sum / (float)s.cols + p.eps);
+  if (here && p.rstd && a.lane == 0) p.rstd[row] = rstd;
+  const T* again = residual ? h : x;
+  auto normed = [&](uint32_t round, int i, float (&f)[8]) {
+    const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
+    const int64_t n = (int64_t)s.cols - (int64_t)c * 8;
+    float w[8];
+    weights_at(p.weight, p.wtype, (uint64_t)c * 8, n, w);
+    if (s.rounds > 1) v[i] = load_eight(again + (uint64_t)c * 8, n);
+    widen(v[i], f);
+#pragma unroll
+    for (int j = 0; j < 8; j++) f[j] = f[j] * rstd * w[j];
+  };
+  if constexpr (!EIGHT_BITS) {
+    T* y = (T*)p.y + row * s.cols;
+    for (uint32_t round = 0; round < s.rounds; round++)
+#pragma unroll
+      for (int i = 0; i < PIECES; i++) {
+        const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
+        float f[8];
+        normed(round, i, f);
+        if (here)
+          store_eight(y + (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8, narrow<T>(f));
+      }
+  } else {
+    uint32_t m = 0;
+    float f[PIECES][8];
+    for (uint32_t round = 0; round < s.rounds; round++)
+#pragma unroll
+      for (int i = 0; i < PIECES; i++) {
+        normed(round, i, f[i]);
+        const uint32_t n = magnitude_of_floats(f[i]);
+        m = m > n ? m : n;
+      }
+    const RowScale r = row_scale(max_over_row(m, s.shift, tops));
+    if (!here) return;
+    uint8_t* codes = (uint8_t*)p.y + row * s.chunks * 8;
+    for (uint32_t round = 0; round < s.rounds; round++)
+#pragma unroll
+      for (int i = 0; i < PIECES; i++) {
+        const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
+        if (s.rounds > 1) normed(round, i, f[i]);
+        if (c < s.chunks)
+          *reinterpret_cast<uint2*>(codes + (uint64_t)c * 8) = code_row_eight(f[i], r.by);
+      }
+    if (a.lane == 0) p.scales[row] = r.scale;
+  }
+}
+
+// ---------------------------------------------------------------- gradients
+
+struct Back {
+  const void *dy, *h, *dh, *weight;
+  const float* rstd;
+  int wtype;
+  void* dx;
+  float* parts;  // dweight's parts [gridDim * slots][cols]; NULL: another kernel sums it
+};
+
+// A workgroup takes every gridDim-th set of rows and adds up what they give to
+// dweight in registers.
+template <typename T, int PIECES>
+__global__ __launch_bounds__(kRowThreads) void rms_norm_back(const Back p, RowShape s) {
+  __shared__ float sums[2][kRowWaves];
+  const uint32_t slots = kRowThreads >> s.shift;
+  const uint64_t sets = (s.rows + slots - 1) / slots;
+  float dw[PIECES][8] = {};
+  uint32_t turn = 0;
+  for (uint64_t set = blockIdx.x; set < sets; set += gridDim.x, turn ^= 1) {
+    const RowAt a = row_at(s, set);
+    const bool here = a.row < s.rows;
+    const uint64_t at = (here ? a.row : s.rows - 1) * s.cols;
+    const float rstd = p.rstd[here ? a.row : s.rows - 1];
+    const T *dy = (const T*)p.dy + at, *h = (const T*)p.h + at;
+    Eight<T> d[PIECES], v[PIECES];
+    auto load = [&](uint32_t round) {
+#pragma unroll
+      for (int i = 0; i < PIECES; i++) {
+        const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
+        const int64_t n = here ? (int64_t)s.cols - (int64_t)c * 8 : 0;
+        d[i] = load_eight(dy + (uint64_t)c * 8, n);
+        v[i] = load_eight(h + (uint64_t)c * 8, n);
+      }
+    };
+    float dot = 0;
+    for (uint32_t round = 0; round < s.rounds; round++) {
+      load(round);
+#pragma unroll
+      for (int i = 0; i < PIECES; i++) {
+        const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
+        float f[8], g[8], w[8];
+        widen(d[i], f);
+        widen(v[i], g);
+        weights_at(p.weight, p.wtype, (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8, w);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          const float n = g[j] * rstd;
+          dot += f[j] * w[j] * n;
+          dw[i][j] += f[j] * n;
+        }
+      }
+    }
+    // two sets of words in turn: a wave may be one row ahead of another
+    dot = sum_over_row(dot, s.shift, sums[turn]) / (float)s.cols;
+    if (here)
+      for (uint32_t round = 0; round < s.rounds; round++) {
+        if (s.rounds > 1) load(round);
+#pragma unroll
+        for (int i = 0; i < PIECES; i++) {
+          const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
+          const int64_t n = (int64_t)s.cols - (int64_t)c * 8;
+          float f[8], g[8], w[8], o[8] = {};
+          widen(d[i], f);
+          widen(v[i], g);
+          weights_at(p.weight, p.wtype, (uint64_t)c * 8, n, w);
+          if (p.dh) widen(load_eight((const T*)p.dh + at + (uint64_t)c * 8, n), o);
+#pragma unroll
+          for (int j = 0; j < 8; j++) o[j] += rstd * (f[j] * w[j] - g[j] * rstd * dot);
+          store_eight((T*)p.dx + at + (uint64_t)c * 8, n, narrow<T>(o));
+        }
+      }
+  }
+  if (!p.parts) return;
+  const uint32_t lanes = 1u << s.shift, lane = threadIdx.x & (lanes - 1);
+  float* to = p.parts + ((uint64_t)blockIdx.x * slots + (threadIdx.x >> s.shift)) * s.cols;
+#pragma unroll
+  for (int i = 0; i < PIECES; i++) {
+    const uint64_t c = (uint64_t)(i * lanes + lane) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+      if (c + j < s.cols) to[c + j] = dw[i][j];
+  }
+}
+
+constexpr uint32_t kSumCols = 32, kSumSlices = 32;
+
+// Column sums of [parts][cols]: 32 columns a workgroup, their rows in 32 slices
+// that are joined in order.
+struct PartRows {
+  const float* parts;
+  uint64_t rows;
+  uint32_t cols;
+  __device__ float at(uint64_t r, uint32_t c) const { return parts[r * cols + c]; }
+};
+// The same of dy times n, where a row is too long for one workgroup's registers.
+template <typename T>
+struct GradientRows {
+  const T *dy, *h;
+  const float* rstd;
+  uint64_t rows;
+  uint32_t cols;
+  __device__ float at(uint64_t r, uint32_t c) const {
+    return (float)dy[r * cols + c] * ((float)h[r * cols + c] * rstd[r]);
+  }
+};
+template <typename F>
+__global__ __launch_bounds__(kSumCols* kSumSlices) void column_sums(const F from, void* to,
+                                                                    int type) {
+  __shared__ float part[kSumSlices][kSumCols + 1];
+  const uint32_t col = threadIdx.x % kSumCols, slice = threadIdx.x / kSumCols;
+  const uint64_t c = (uint64_t)blockIdx.x * kSumCols + col;
+  float sum = 0;
+  if (c < from.cols)
+    for (uint64_t r = slice; r < from.rows; r += kSumSlices) sum += from.at(r, (uint32_t)c);
+  part[slice][col] = sum;
+  __syncthreads();
+  if (slice || c >= from.cols) return;
+  sum = 0;
+  for (uint32_t i = 0; i < kSumSlices; i++) sum += part[i][col];
+  if (type == EC_TYPE_F32) ((float*)to)[c] = sum;
+  else if (type == EC_TYPE_F16) ((f16_t*)to)[c] = (f16_t)sum;
+  else ((bf16_t*)to)[c] = (bf16_t)sum;
+}
+
+// ---------------------------------------------------------------- host
+
+ec_status launched() { return hipGetLastError() == hipSuccess ? EC_OK : EC_ERR_DEVICE; }
+bool fine(const void* p, size_t to) { return p && aligned(p, to); }
+
+// What forward and backward ask of sizes and types.
+ec_status check(int type, int wtype, uint64_t rows, uint64_t cols) {
+  if (!type_known(type) || !type_known(wtype) || cols == 0) return EC_ERR_INVALID;
+  return rows > EC_MX_MAX_ROWS || cols > EC_MX_MAX_DEPTH ? EC_ERR_UNSUPPORTED : EC_OK;
+}
+
+ec_status check_norm(const Norm& p, int type, uint64_t rows, uint64_t cols) {
+  const ec_status st = check(type, p.wtype, rows, cols);
+  if (st != EC_OK) return st;
+  if (p.stride < cols || (!p.residual) != (!p.h) || (p.residual && p.residual_stride < cols) ||
+      !(p.eps > 0) || !std::isfinite(p.eps))
+    return EC_ERR_INVALID;
+  if (rows == 0) return EC_OK;
+  const size_t b = type_bytes(type);
+  return fine(p.x, b) && aligned(p.residual, b) && aligned(p.h, b) &&
+                 fine(p.weight, type_bytes(p.wtype)) && aligned(p.rstd, 4)
+             ? EC_OK
+             : EC_ERR_INVALID;
+}
+
+template <typename T, bool EIGHT_BITS>
+ec_status norm_as(const Norm& p, uint64_t rows, uint64_t cols, hipStream_t stream) {
+  uint32_t pieces;
+  const RowShape s =
+      row_shape(rows, cols, EIGHT_BITS ? ec_mx_padded(cols) / 8 : ceil_div(cols, 8), pieces);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid_of(row_blocks(s)), dim3(kRowThreads), 0, stream, p, s);
+  };
+  switch (pieces) {
+    case 1: go(rms_norm<T, 1, EIGHT_BITS>); break;
+    case 2: go(rms_norm<T, 2, EIGHT_BITS>); break;
+    case 4: go(rms_norm<T, 4, EIGHT_BITS>); break;
+    default: go(rms_norm<T, 8, EIGHT_BITS>);
+  }
+  return launched();
+}
+template <bool EIGHT_BITS>
+ec_status norm(const Norm& p, int type, uint64_t rows, uint64_t cols, hipStream_t s) {
+  switch (type) {
+    case EC_TYPE_F32: return norm_as<float, EIGHT_BITS>(p, rows, cols, s);
+    case EC_TYPE_F16: return norm_as<f16_t, EIGHT_BITS>(p, rows, cols, s);
+    default: return norm_as<bf16_t, EIGHT_BITS>(p, rows, cols, s);
+  }
+}
+
+// Workgroups of the backward pass: two rows a slot at least, so that dweight's
+// parts stay below half of dy's elements.
+uint32_t back_blocks(const RowShape& s) {
+  const uint64_t sets = ceil_div(s.rows, kRowThreads >> s.shift), n = ceil_div(sets, 2);
+  return (uint32_t)(n > 1024 ? 1024 : n);
+}
+
+template <typename T>
+ec_status back_as(Back p, uint64_t rows, uint64_t cols, void* dweight, void* workspace,
+                  hipStream_t stream) {
+  uint32_t pieces;
+  const RowShape s = row_shape(rows, cols, ceil_div(cols, 8), pieces);
+  p.parts = s.rounds == 1 ? (float*)workspace : nullptr;
+  const uint32_t blocks = back_blocks(s);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kRowThreads), 0, stream, p, s);
+  };
+  if (rows) switch (pieces) {
+      case 1: go(rms_norm_back<T, 1>); break;
+      case 2: go(rms_norm_back<T, 2>); break;
+      case 4: go(rms_norm_back<T, 4>); break;
+      default: go(rms_norm_back<T, 8>);
+    }
+  const dim3 grid((uint32_t)ceil_div(cols, kSumCols)), block(kSumCols * kSumSlices);
+  if (p.parts || !rows) {
+    const PartRows f{p.parts, rows ? blocks * (uint64_t)(kRowThreads >> s.shift) : 0, s.cols};
+    hipLaunchKernelGGL((column_sums<PartRows>), grid, block, 0, stream, f, dweight, p.wtype);
+  } else {
+    const GradientRows<T> f{(const T*)p.dy, (const T*)p.h, p.rstd, rows, s.cols};
+    hipLaunchKernelGGL((column_sums<GradientRows<T>>), grid, block, 0, stream, f, dweight,
+                       p.wtype);
+  }
+  return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+ec_status ec_rms_norm(const void* x, uint64_t stride, const void* residual,
+                      uint64_t residual_stride, int type, uint64_t rows, uint64_t cols,
+                      const void* weight, int wtype, float eps, void* h, void* y, float* rstd,
+                      void* stream) {
+  const Norm p{x, residual, weight, stride, residual_stride, wtype, eps, h, y, nullptr, rstd};
+  const ec_status st = check_norm(p, type, rows, cols);
+  if (st != EC_OK || rows == 0) return st;
+  if (!fine(y, type_bytes(type))) return EC_ERR_INVALID;
+  return norm<false>(p, type, rows, cols, (hipStream_t)stream);
+}
+
+ec_status ec_rms_norm_i8(const void* x, uint64_t stride, const void* residual,
+                         uint64_t residual_stride, int type, uint64_t rows, uint64_t cols,
+                         const void* weight, int wtype, float eps, void* h, void* codes,
+                         void* scales, void* stream) {
+  const Norm p{x,   residual, weight, stride,         residual_stride, wtype,
+               eps, h,        codes,  (float*)scales, nullptr};
+  const ec_status st = check_norm(p, type, rows, cols);
+  if (st != EC_OK || rows == 0) return st;
+  if (!read_ok(codes, scales)) return EC_ERR_INVALID;
+  return norm<true>(p, type, rows, cols, (hipStream_t)stream);
+}
+
+size_t ec_rms_norm_backward_workspace_bytes(uint64_t rows, uint64_t cols) {
+  if (rows == 0 || cols == 0) return 0;
+  uint32_t pieces;
+  const RowShape s = row_shape(rows, cols, ceil_div(cols, 8), pieces);
+  return s.rounds > 1 ? 0 : (size_t)back_blocks(s) * (kRowThreads >> s.shift) * cols * 4;
+}
+
+ec_status ec_rms_norm_backward(const void* dy, const void* h, const void* dh, int type,
+                               uint64_t rows, uint64_t cols, const float* rstd, const void* weight,
+                               int wtype, void* dx, void* dweight, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  const ec_status st = check(type, wtype, rows, cols);
+  if (st != EC_OK) return st;
+  const size_t b = type_bytes(type), wb = type_bytes(wtype);
+  if (!fine(dweight, wb)) return EC_ERR_INVALID;
+  if (rows && (!fine(dy, b) || !fine(h, b) || !aligned(dh, b) || !fine(rstd, 4) ||
+               !fine(weight, wb) || !fine(dx, b)))
+    return EC_ERR_INVALID;
+  const size_t need = ec_rms_norm_backward_workspace_bytes(rows, cols);
+  if (need && !fine(workspace, 16)) return EC_ERR_INVALID;
+  if (workspace_bytes < need) return EC_ERR_CAPACITY;
+  const Back p{dy, h, dh, weight, rstd, wtype, dx, nullptr};
+  hipStream_t s = (hipStream_t)stream;
+  switch (type) {
+    case EC_TYPE_F32: return back_as<float>(p, rows, cols, dweight, workspace, s);
+    case EC_TYPE_F16: return back_as<f16_t>(p, rows, cols, dweight, workspace, s);
+    default: return back_as<bf16_t>(p, rows, cols, dweight, workspace, s);
+  }
+}
+
+}  // extern "C"

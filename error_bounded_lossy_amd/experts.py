@@ -1,6 +1,7 @@
-"""The token exchange of an expert layer on gfx950 (include/ec_experts.h):
-tokens sorted by expert and brought back with weights applied, with the
-gradients of both ways, and a dispatch that sends the 4-bit form of mx.py.
+"""The routing and the token exchange of an expert layer on gfx950
+(include/ec_experts.h): experts chosen by their scores, tokens sorted by expert
+and brought back with weights applied, with the gradients of all of it, and
+dispatches that send the 4-bit form of mx.py or the 8-bit form of i8.py.
 
 Calls run on torch's current stream of the tensors' device, or on `stream`, on
 which the results are then allocated.  Results carry no autograd history: the
@@ -8,10 +9,15 @@ gradients are functions of their own.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _binding as _b
-from .mx import TYPES, MXTensor, _empty, _refuse, _type
+from .i8 import I8Tensor, _empty_i8
+from .mx import TYPES, MXTensor, _empty, _refuse, _rows, _type
+
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 def _ints(t, shape) -> bool:
@@ -37,6 +43,73 @@ class Routing:
     def _set(self, order, place, offsets, tokens, choices, experts):
         self.order, self.place, self.offsets = order, place, offsets
         self.tokens, self.choices, self.experts = tokens, choices, experts
+
+
+def _logits(x, score, scale, what):
+    kind = _type(x, what)
+    if x.dim() != 2 or x.shape[1] == 0 or score not in SCORES:
+        _refuse(f"{what}: logits [tokens, experts] and a score of {sorted(SCORES)} are wanted")
+    if not math.isfinite(scale):
+        _refuse(f"{what}: a finite scale is wanted")
+    return *_rows(x), kind
+
+
+def expert_route(logits: torch.Tensor, choices: int, score: str = "softmax",
+                 bias: torch.Tensor | None = None, groups: int = 1, top_groups: int = 1,
+                 renormalize: bool = True, scale: float = 1.0, stream=None):
+    """(ids, int32 [tokens, choices], weights, float32 [tokens, choices]) of logits [tokens,
+    experts]: the experts with the largest score + bias (float32 [experts]; without a bias the
+    largest logits), the largest first and of equal ones the lowest index, and their scores times
+    scale, divided by the sum of the chosen scores with renormalize.
+
+    score: "softmax" or "sigmoid".  With groups, experts are taken from the top_groups of as many
+    runs of consecutive experts whose two best score + bias sum highest.  An expert whose logit is
+    -inf is not taken: where none is left, the id is -1 (which expert_sort drops) and the weight 0."""
+    if stream is not None or _b.elsewhere(logits):
+        return _b.on_stream(expert_route, (logits, choices, score, bias, groups, top_groups,
+                                           renormalize, scale), stream)
+    r, stride, kind = _logits(logits, score, scale, "expert_route")
+    tokens, experts = r.shape
+    if (groups < 1 or experts % groups or not 0 < top_groups <= groups
+            or not 0 < choices <= experts // groups * top_groups):
+        _refuse("expert_route: groups of as many experts each, and no more choices than experts "
+                "in top_groups of them are wanted")
+    if bias is not None:
+        if bias.dtype != torch.float32 or bias.shape != (experts,) or bias.device != r.device:
+            _refuse("expert_route: a float32 bias [experts] on the logits' device is wanted")
+        bias = bias.contiguous()
+    ids = torch.empty((tokens, choices), dtype=torch.int32, device=r.device)
+    weights = torch.empty((tokens, choices), dtype=torch.float32, device=r.device)
+    _b.check(_b.lib().ec_expert_route(
+        r.data_ptr(), kind, tokens, stride, experts, None if bias is None else bias.data_ptr(),
+        choices, SCORES[score], groups, top_groups, bool(renormalize), scale, ids.data_ptr(),
+        weights.data_ptr(), _b.current_stream(r)), "ec_expert_route")
+    return ids, weights
+
+
+def expert_route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor,
+                          score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                          stream=None) -> torch.Tensor:
+    """dlogits [tokens, experts] of expert_route's weights, from dweights, float32 [tokens,
+    choices], and the ids of the forward pass with its score, renormalize and scale.  Which experts
+    are taken has no gradient, and so neither has the bias."""
+    if stream is not None or _b.elsewhere(logits):
+        return _b.on_stream(expert_route_backward,
+                            (dweights, logits, ids, score, renormalize, scale), stream)
+    r, stride, kind = _logits(logits, score, scale, "expert_route_backward")
+    tokens, experts = r.shape
+    if (not _ints(ids, (tokens, *ids.shape[1:])) or ids.dim() != 2 or ids.shape[1] == 0
+            or dweights.dtype != torch.float32 or dweights.shape != ids.shape
+            or not ids.device == dweights.device == r.device):
+        _refuse("expert_route_backward: int32 ids and float32 dweights [tokens, choices] on the "
+                "logits' device are wanted")
+    dweights = dweights.contiguous()
+    dlogits = torch.empty((tokens, experts), dtype=r.dtype, device=r.device)
+    _b.check(_b.lib().ec_expert_route_backward(
+        dweights.data_ptr(), r.data_ptr(), kind, tokens, stride, experts, ids.data_ptr(),
+        ids.shape[1], SCORES[score], bool(renormalize), scale, dlogits.data_ptr(),
+        _b.current_stream(r)), "ec_expert_route_backward")
+    return dlogits
 
 
 def expert_sort(ids: torch.Tensor, experts: int, stream=None) -> Routing:
@@ -117,6 +190,21 @@ def expert_dispatch_mx(x: torch.Tensor, routing: Routing, stream=None) -> MXTens
                                             r.place.data_ptr(), r.choices, r.offsets.data_ptr(),
                                             r.experts, at, at + q._split,
                                             _b.current_stream(x)), "ec_expert_dispatch_mx")
+    return q
+
+
+def expert_dispatch_i8(x: I8Tensor, routing: Routing, stream=None) -> I8Tensor:
+    """The same of tokens that are in the 8-bit form, as rms_norm_i8 makes them: x [tokens, cols]."""
+    if stream is not None or _b.elsewhere(x.codes):
+        return _b.on_stream(expert_dispatch_i8, (x, routing), stream)
+    r = routing
+    if (len(x.lead) != 1 or x.lead[0] != r.tokens or x.cols == 0 or not x.codes.is_cuda
+            or x.codes.device != r.place.device):
+        _refuse("expert_dispatch_i8: rows [tokens, cols] on the routing's device are wanted")
+    q = _empty_i8((r.tokens * r.choices,), x.cols, x.codes)
+    _b.check(_b.lib().ec_expert_dispatch_i8(
+        *x.pointers(), r.tokens, x.padded, r.place.data_ptr(), r.choices, r.offsets.data_ptr(),
+        r.experts, *q.pointers(), _b.current_stream(x.codes)), "ec_expert_dispatch_i8")
     return q
 
 

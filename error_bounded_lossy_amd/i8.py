@@ -1,0 +1,166 @@
+"""The 8-bit integer form on gfx950 (include/ec_i8.h): rows of whole numbers
+with one scale each, and products of them on the matrix cores.
+
+Calls run on torch's current stream of the tensors' device, or on `stream`, on
+which the results are then allocated.  Results carry no autograd history: the
+form is for serving (training has the block scales of mx.py).
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import _binding as _b
+from .mx import TYPES, _offsets, _refuse, _rows, _type
+
+
+class I8Tensor:
+    """A tensor in the 8-bit form along its last dimension, of `cols` elements: codes, int8
+    [..., padded] with zeros from cols on, and scales, float32 [...]."""
+
+    __slots__ = ("codes", "scales", "cols", "padded", "lead")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
+        p = (cols + 127) // 128 * 128
+        if (codes.dtype != torch.int8 or scales.dtype != torch.float32 or cols < 0
+                or codes.dim() == 0 or codes.shape[-1] != p or scales.shape != codes.shape[:-1]
+                or not codes.is_contiguous() or not scales.is_contiguous()
+                or codes.device != scales.device):
+            _refuse("I8Tensor: int8 codes [..., padded] and float32 scales [...], contiguous and "
+                    "on one device, are wanted")
+        self.codes, self.scales, self.cols, self.padded = codes, scales, cols, p
+        self.lead = codes.shape[:-1]
+
+    def __reduce__(self):
+        return I8Tensor, (self.codes, self.scales, self.cols)
+
+    def pointers(self) -> tuple[int, int]:
+        """Where codes and scales are now (a caller may replace their memory, not their form)."""
+        codes, scales = self.codes, self.scales
+        if (codes.numel() != scales.numel() * self.padded or codes.shape[:-1] != self.lead
+                or not codes.is_contiguous() or not scales.is_contiguous()):
+            _refuse("I8Tensor: its memory was replaced by some of another form")
+        return codes.data_ptr(), scales.data_ptr()
+
+    @property
+    def shape(self) -> torch.Size:
+        return torch.Size((*self.lead, self.cols))
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    def numel_bytes(self) -> int:
+        return math.prod(self.lead) * (self.padded + 4)
+
+
+def _empty_i8(lead, cols, like) -> I8Tensor:
+    q = object.__new__(I8Tensor)  # of these there is nothing to check
+    q.cols, q.padded, q.lead = cols, (cols + 127) // 128 * 128, torch.Size(lead)
+    q.codes = like.new_empty((*lead, q.padded), dtype=torch.int8)
+    q.scales = like.new_empty(lead, dtype=torch.float32)
+    return q
+
+
+def i8_quantize(x: torch.Tensor, stream=None) -> I8Tensor:
+    """x [..., cols] in the 8-bit form along its last dimension, one scale a row."""
+    if stream is not None or _b.elsewhere(x):
+        return _b.on_stream(i8_quantize, (x,), stream)
+    kind = _type(x, "i8_quantize")
+    if x.dim() == 0 or x.shape[-1] == 0:
+        _refuse("i8_quantize: at least one element a row is wanted")
+    r, stride = _rows(x)
+    q = _empty_i8(x.shape[:-1], x.shape[-1], x)
+    _b.check(_b.lib().ec_i8_quantize(r.data_ptr(), kind, r.shape[0], r.shape[1], stride,
+                                     *q.pointers(), _b.current_stream(x)), "ec_i8_quantize")
+    return q
+
+
+def i8_dequantize(q: I8Tensor, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+    """The values that q holds, rounded once to dtype."""
+    if stream is not None or _b.elsewhere(q.codes):
+        return _b.on_stream(i8_dequantize, (q, dtype), stream)
+    kind = TYPES.get(dtype)
+    if kind is None or not q.codes.is_cuda or q.cols == 0:
+        _refuse("i8_dequantize: a nonempty row on the GPU and float32, float16 or bfloat16 are wanted")
+    y = q.codes.new_empty((*q.lead, q.cols), dtype=dtype)
+    _b.check(_b.lib().ec_i8_dequantize(*q.pointers(), q.scales.numel(), q.cols, y.data_ptr(), kind,
+                                       q.cols, _b.current_stream(y)), "ec_i8_dequantize")
+    return y
+
+
+def i8_product(a: I8Tensor, b: I8Tensor, dtype: torch.dtype = torch.bfloat16,
+               stream=None) -> torch.Tensor:
+    """a b^T [rows, cols] of a [rows, depth] and b [cols, depth], summed in whole numbers."""
+    if stream is not None or _b.elsewhere(a.codes):
+        return _b.on_stream(i8_product, (a, b, dtype), stream)
+    kind = TYPES.get(dtype)
+    if (kind is None or len(a.lead) != 1 or len(b.lead) != 1 or a.cols != b.cols or a.cols == 0
+            or b.lead[0] == 0 or not a.codes.is_cuda or a.codes.device != b.codes.device):
+        _refuse("i8_product: [rows, depth] and [cols, depth] on one GPU are wanted")
+    rows, cols = a.lead[0], b.lead[0]
+    y = a.codes.new_empty((rows, cols), dtype=dtype)
+    _b.check(_b.lib().ec_i8_product(*a.pointers(), rows, *b.pointers(), cols, a.padded,
+                                    y.data_ptr(), kind, _b.current_stream(y)), "ec_i8_product")
+    return y
+
+
+def i8_experts_product(a: I8Tensor, b: I8Tensor, offsets: torch.Tensor,
+                       dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """Rows a [rows, depth] sorted by expert, rows [offsets[e], offsets[e + 1]) times the weights of
+    expert e, b [experts, cols, depth]; zeros in rows of no expert."""
+    if stream is not None or _b.elsewhere(a.codes):
+        return _b.on_stream(i8_experts_product, (a, b, offsets, dtype), stream)
+    kind = TYPES.get(dtype)
+    if (kind is None or len(a.lead) != 1 or len(b.lead) != 2 or a.cols != b.cols or a.cols == 0
+            or 0 in b.lead or not a.codes.is_cuda or a.codes.device != b.codes.device):
+        _refuse("i8_experts_product: [rows, depth] and [experts, cols, depth] on one GPU are wanted")
+    experts, cols = b.lead
+    _offsets(offsets, experts, a.codes.device, "i8_experts_product")
+    rows = a.lead[0]
+    y = a.codes.new_empty((rows, cols), dtype=dtype)
+    _b.check(_b.lib().ec_i8_product_experts(*a.pointers(), rows, *b.pointers(), cols, a.padded,
+                                            offsets.data_ptr(), experts, y.data_ptr(), kind,
+                                            _b.current_stream(y)), "ec_i8_product_experts")
+    return y
+
+
+def _linear(x, w, offsets, experts, what):
+    kind = _type(x, what)
+    cols, depth = w.lead[-1], x.shape[-1]
+    if w.cols != depth or depth == 0 or 0 in w.lead or w.codes.device != x.device:
+        _refuse(f"{what}: weights [.., cols, depth] on the device of x [.., depth] are wanted")
+    r, stride = _rows(x)
+    rows = r.shape[0]
+    L = _b.lib()
+    y = x.new_empty((*x.shape[:-1], cols))
+    need = L.ec_i8_linear_workspace_bytes(rows, depth, cols, experts)
+    # held until the call is back: before, its kernels are not all enqueued
+    ws = w.codes.new_empty(need) if need else None
+    _b.check(L.ec_i8_linear(r.data_ptr(), kind, rows, depth, stride, *w.pointers(), cols,
+                            offsets.data_ptr() if experts else None, experts, y.data_ptr(),
+                            ws.data_ptr() if need else None, need,
+                            _b.current_stream(x)), "ec_i8_linear")
+    return y
+
+
+def i8_linear(x: torch.Tensor, w: I8Tensor, stream=None) -> torch.Tensor:
+    """x w^T with x [..., depth] quantized on the way, one scale a row, and weights w [cols, depth]
+    with one scale an output channel."""
+    if stream is not None or _b.elsewhere(x):
+        return _b.on_stream(i8_linear, (x, w), stream)
+    if len(w.lead) != 1 or x.dim() == 0:
+        _refuse("i8_linear: x [.., depth] and weights [cols, depth] are wanted")
+    return _linear(x, w, None, 0, "i8_linear")
+
+
+def i8_experts_linear(x: torch.Tensor, w: I8Tensor, offsets: torch.Tensor,
+                      stream=None) -> torch.Tensor:
+    """i8_experts_product of rows x [rows, depth] that are quantized on the way."""
+    if stream is not None or _b.elsewhere(x):
+        return _b.on_stream(i8_experts_linear, (x, w, offsets), stream)
+    if len(w.lead) != 2 or x.dim() != 2:
+        _refuse("i8_experts_linear: x [rows, depth] and weights [experts, cols, depth] are wanted")
+    _offsets(offsets, w.lead[0], x.device, "i8_experts_linear")
+    return _linear(x, w, offsets, w.lead[0], "i8_experts_linear")
