@@ -166,3 +166,31 @@ def test_many_tokens(choices):
     want = torch.where(order.values[:, :choices] > -math.inf, order.indices[:, :choices], -1)
     assert torch.equal(i.long(), want)
     assert torch.allclose(w.sum(1), (i >= 0).any(1).float(), atol=1e-6)
+
+
+@pytest.mark.parametrize("tokens", [40, 5000])
+@pytest.mark.parametrize("experts,groups,top", [(64, 1, 1), (256, 8, 4), (40, 4, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scores_next_to_each_other_go_by_64_bits(score, experts, groups, top, tokens):
+    # score + bias differ by parts of a unit of 32 bits, in clusters longer than the choices, or are equal
+    g = torch.Generator("cuda").manual_seed(experts)
+    l = torch.randn(tokens, experts, generator=g, device="cuda") * torch.rand(tokens, 1, generator=g, device="cuda") * 1e-6
+    l[::3] = (l[::3] * 1e6).round() / 4
+    l += torch.randn(tokens, 1, generator=g, device="cuda")
+    bias = 1e-9 * torch.randint(-3, 4, (experts,), generator=g, device="cuda").float()
+    s = torch.softmax(l.double(), 1) if score == "softmax" else 1 / (1 + torch.exp(-l.double()))
+    by = s + bias.double()
+    if groups > 1:
+        best = by.unflatten(1, (groups, -1)).sort(-1, descending=True).values[..., :2].sum(-1)
+        kept = torch.sort(best, dim=1, descending=True, stable=True).indices[:, :top]
+        inside = torch.zeros_like(best, dtype=torch.bool).scatter_(1, kept, True)
+        by = torch.where(inside[..., None], by.unflatten(1, (groups, -1)), -math.inf).flatten(1)
+    got, _ = ec.expert_route(l, 7, score, bias, groups, top)
+    # equal in one program's 64 bits may be a unit apart in another's: what is taken has to be as large
+    mine = by.gather(1, got.long())
+    want = torch.sort(by, dim=1, descending=True, stable=True)
+    assert ((mine - want.values[:, :7]).abs() <= 4e-16 * (1 + mine.abs())).all()
+    assert (got.sort(1).values.diff(dim=1) > 0).all()
+    # without a bias the logits decide, exactly
+    got, _ = ec.expert_route(l, 7, score)
+    assert torch.equal(got.long(), torch.sort(l, dim=1, descending=True, stable=True).indices[:, :7])
