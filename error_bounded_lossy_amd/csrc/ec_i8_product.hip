@@ -10,8 +10,6 @@ using namespace ecmx;
 
 namespace {
 
-typedef int i32x16 __attribute__((ext_vector_type(16)));
-
 enum { kDense = 0, kExperts = 1 };
 
 struct Operand {
@@ -33,28 +31,25 @@ struct Product {
 // ---------------------------------------------------------------- tiles
 
 // One workgroup of 2 by 2 waves computes a tile of 64 FM rows by 64 FN columns,
-// a wave 32 FM by 32 FN of it with 32x32x32 instructions.  With FM = FN = 4 a
-// wave's sums fill half of its 512 registers, and an operand byte read from LDS
-// is used 128 times.
+// a wave 32 FM by 32 FN of it with 16x16x64 instructions, which on random codes
+// reach 4.0 POP/s where those of 32x32x32 reach 3.3 (the clock falls with the
+// power; 4.9 and 4.6 on zeros).  With FM = FN = 4 a wave's sums fill half of its
+// 512 registers, and an operand byte read from LDS is used 128 times.
 //
-// A stage is 64 codes of every row of both operands, brought to LDS without
-// passing registers.  Four stages are in LDS: one is multiplied while the loads
-// of the next three fly, with one barrier a stage, placed before the last
-// multiplications so that they cover the first reads of the next stage.
+// A stage is 128 codes of every row of both operands, a line of the caches, so
+// that a line is asked for once.  It is brought to LDS without passing registers,
+// while the stage before is multiplied (of small tiles, the three before), with
+// one barrier a stage, placed between its two steps so that the second covers the
+// first reads of the next stage.
 //
 // The order within the contraction is free as long as both operands agree, so
-// lane group g of instruction step s takes the 16-byte chunk 2 g + s of a row.
-// Chunks are stored at their number xor bits 1 and 2 of the row, so that 8 lanes
-// of consecutive rows read 8 different 16-byte columns of 128.
+// lane group g of step s takes the 16-byte chunk 4 s + g of a row.
+// Chunks are stored at their number xor the row's lowest three bits, so that 8
+// lanes of consecutive rows read 8 different 16-byte columns of 128.
 template <int BM, int BN>
 struct Stage {
-  uint8_t a[BM * 64];
-  uint8_t b[BN * 64];
-};
-
-template <int FM, int FN>
-struct Fragments {
-  i32x4 a[FM], b[FN];
+  uint8_t a[BM * 128];
+  uint8_t b[BN * 128];
 };
 
 // Where this lane reads in a stage: step 0's chunk of its first rows.
@@ -62,43 +57,72 @@ struct Lane {
   uint32_t a, b;
 };
 
-template <int BM, int BN, int FM, int FN>
-__device__ __forceinline__ void read(const Stage<BM, BN>& st, const Lane& at, int step,
-                                     Fragments<FM, FN>& f) {
-  // chunk 2 g + 1 lies at the place of chunk 2 g with the lowest bit turned
+// Fragment i of a step.
+template <typename St>
+__device__ __forceinline__ i32x4 read_a(const St& st, const Lane& at, int step, int i) {
+  return *reinterpret_cast<const i32x4*>(st.a + (at.a ^ (step << 6)) + i * 2048);
+}
+template <int N, typename St>
+__device__ __forceinline__ void read_b(const St& st, const Lane& at, int step, i32x4 (&b)[N]) {
 #pragma unroll
-  for (int i = 0; i < FN; i++)
-    f.b[i] = *reinterpret_cast<const i32x4*>(st.b + (at.b ^ (step << 4)) + i * 2048);
-#pragma unroll
-  for (int i = 0; i < FM; i++)
-    f.a[i] = *reinterpret_cast<const i32x4*>(st.a + (at.a ^ (step << 4)) + i * 2048);
+  for (int i = 0; i < N; i++)
+    b[i] = *reinterpret_cast<const i32x4*>(st.b + (at.b ^ (step << 6)) + i * 2048);
 }
 
-// `between(i)` issues what goes between the rows of multiplications; nothing
-// else is moved there.
-template <int FM, int FN, typename F>
-__device__ __forceinline__ void multiply(const Fragments<FM, FN>& f, i32x16 (&acc)[FM][FN],
-                                         F&& between) {
+// `between(i)` issues what goes behind row i of the multiplications, when a[i] is
+// free; nothing else is moved there.
+//
+// The sums of the largest tile (64 results) are held in the accumulation registers
+// by the instruction's own operands: from the builtin, the compiler moves most of
+// them to other registers and back in every round of the loop (8192^3 625 us).
+// What it does not see are the waits between the instruction and what uses its
+// result: none are due among multiplications, 64 of which are between two of one
+// result; the barrier is between the zeros and the first of them, and finished()
+// waits before the results are read.
+__device__ __forceinline__ void multiply_held(i32x4& acc, const i32x4& b, const i32x4& a) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+}
+template <int M, int N>
+__device__ __forceinline__ void hold(i32x4 (&acc)[M][N]) {  // keeps its place among such statements
 #pragma unroll
-  for (int i = 0; i < FM; i++) {
+  for (int i = 0; i < M; i++)
+#pragma unroll
+    for (int j = 0; j < N; j++) asm volatile("" : "+a"(acc[i][j]));
+}
+template <int M, int N>
+__device__ __forceinline__ void finished(i32x4 (&acc)[M][N]) {
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  hold(acc);
+}
+
+template <int M, int N, typename F>
+__device__ __forceinline__ void multiply(const i32x4 (&a)[M], const i32x4 (&b)[N],
+                                         i32x4 (&acc)[M][N], F&& between) {
+#pragma unroll
+  for (int i = 0; i < M; i++) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < FN; j++)
-      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < N; j++) {
+      if constexpr (M * N == 64) multiply_held(acc[i][j], b[j], a[i]);
+      else acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[j], a[i], acc[i][j], 0, 0, 0);
+    }
     __builtin_amdgcn_sched_barrier(0);
     between(i);
   }
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int FM, int FN, typename T, int MODE, bool PAST>
-__global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void i8_tiles(const Product p) {
+// STAGES: 2 of the largest tile (of one line each they fill LDS) and where two
+// workgroups share a unit; 4 where there is a unit for each, or the tile is small.
+template <int FM, int FN, int STAGES, typename T, int MODE, bool PAST>
+__global__ __launch_bounds__(256, STAGES * FM * FN >= 16 ? 1 : 2) void i8_tiles(const Product p) {
   constexpr int BM = 64 * FM, BN = 64 * FN, kWaves = 4;
   using St = Stage<BM, BN>;
   constexpr uint32_t kShift = FM == 1 ? 6 : FM == 2 ? 7 : 8;
   static_assert((1u << kShift) == BM, "tile rows");
-  // four variables, not an array: the compiler then knows which loads a read waits for
-  __shared__ __attribute__((aligned(16))) St st0, st1, st2, st3;
+  // (variables, not an array: the compiler then knows which loads a read waits for)
+  __shared__ __attribute__((aligned(16))) St st0, st1;
+  __shared__ __attribute__((aligned(16))) std::conditional_t<STAGES == 4, St, int> st2, st3;
   __shared__ __attribute__((aligned(16))) float scales[BM + BN];  // of a's rows, then of b's
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t wm = wave & 1, wn = wave >> 1;
@@ -111,8 +135,9 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void i8_tiles(const Produ
   // in an XCD's run, 8 tiles along the rows share a column tile
   const uint32_t width = 8 * p.n_tiles, band = t / width;
   const uint32_t high = min(m_tiles - band * 8, 8u);
-  const uint32_t tm = band * 8 + (t - band * width) % high;
-  const uint32_t tn = (t - band * width) / high;
+  // (as scalars: a buffer whose address is in vector registers costs a loop a load)
+  const uint32_t tm = __builtin_amdgcn_readfirstlane(band * 8 + (t - band * width) % high);
+  const uint32_t tn = __builtin_amdgcn_readfirstlane((t - band * width) / high);
 
   // this tile's rows [m0, m_end) of a and y, and its columns
   uint64_t m0 = (uint64_t)tm * BM, m_end = p.rows;
@@ -139,113 +164,134 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void i8_tiles(const Produ
     bs += (uint64_t)gt.group * p.cols;
   }
 
-  // What this lane loads: of instruction q of an operand, row 16 q + lane / 4
-  // and chunk (lane & 3) xor bits 1 and 2 of the row.  Rows past the end read
-  // the last one: they only reach results that are not stored.
+  // What this lane loads: of instruction q of an operand, row 8 q + lane / 8 and
+  // chunk (lane & 7) xor the row's lowest three bits.  Rows past the end read the
+  // last one: they only reach results that are not stored.
   const uint32_t pitch = p.depth;
   const uint32_t m_last = (uint32_t)(m_end - m0) - 1, n_last = p.cols - n0 - 1;
-  const uint32_t chunk = (lane & 3) ^ ((lane >> 3) & 3);
+  const uint32_t chunk = (lane & 7) ^ (lane >> 3);
   // offsets from the tile's first row: at most 256 rows of 2^17 bytes
-  constexpr int LA = BM / 16 / kWaves, LB = BN / 16 / kWaves;  // a wave's loads of a stage
+  constexpr int LA = BM / 8 / kWaves, LB = BN / 8 / kWaves;  // a wave's loads of a stage
   uint32_t oa[LA], ob[LB];
 #pragma unroll
   for (int i = 0; i < LA; i++)
-    oa[i] = min((wave * LA + i) * 16 + (lane >> 2), m_last) * pitch + chunk * 16;
+    oa[i] = min((wave * LA + i) * 8 + (lane >> 3), m_last) * pitch + chunk * 16;
 #pragma unroll
   for (int i = 0; i < LB; i++)
-    ob[i] = min((wave * LB + i) * 16 + (lane >> 2), n_last) * pitch + chunk * 16;
+    ob[i] = min((wave * LB + i) * 8 + (lane >> 3), n_last) * pitch + chunk * 16;
   constexpr int kLoads = LA + LB;
-  const uint32_t stages = __builtin_amdgcn_readfirstlane(p.depth / 64), fours = stages / 4;
+  const uint32_t stages = __builtin_amdgcn_readfirstlane(p.depth / 128);
   // Past the last stage it is loaded again, so that every turn below does the
-  // same and waits for the same number of loads.  Part i of FM.
+  // same and waits for the same number of loads.  Part i of 2 FM: two loads behind every row
+  // of multiplications (8192^3: 494 us; four behind the first half of them 509, eight
+  // behind the first quarter 530).
   const __amdgpu_buffer_rsrc_t ra = buffer_at(p.a.codes + m0 * pitch);
   const __amdgpu_buffer_rsrc_t rb = buffer_at(bc + (uint64_t)n0 * pitch);
   auto load = [&](St& st, uint32_t stage, int part) {
-    const uint32_t c = __builtin_amdgcn_readfirstlane(min(stage, stages - 1)) * 64;
+    const uint32_t c = __builtin_amdgcn_readfirstlane(min(stage, stages - 1)) * 128;
 #pragma unroll
-    for (int i = part * LA / FM; i < (part + 1) * LA / FM; i++)
+    for (int i = part * LA / (2 * FM); i < (part + 1) * LA / (2 * FM); i++)
       to_lds16(ra, oa[i], c, st.a + (wave * LA + i) * 1024);
 #pragma unroll
-    for (int i = part * LB / FM; i < (part + 1) * LB / FM; i++)
+    for (int i = part * LB / (2 * FM); i < (part + 1) * LB / (2 * FM); i++)
       to_lds16(rb, ob[i], c, st.b + (wave * LB + i) * 1024);
   };
   auto load_all = [&](St& st, uint32_t stage) {
 #pragma unroll
-    for (int i = 0; i < FM; i++) load(st, stage, i);
+    for (int i = 0; i < 2 * FM; i++) load(st, stage, i);
   };
 
-  const uint32_t r = lane & 31, g = lane >> 5;
+  const uint32_t r = lane & 15, g = lane >> 4;
   Lane at;
-  at.a = (wm * 32 * FM + r) * 64 + ((2 * g) ^ ((r >> 1) & 3)) * 16;
-  at.b = (wn * 32 * FN + r) * 64 + ((2 * g) ^ ((r >> 1) & 3)) * 16;
+  at.a = (wm * 32 * FM + r) * 128 + (g ^ (r & 7)) * 16;
+  at.b = (wn * 32 * FN + r) * 128 + (g ^ (r & 7)) * 16;
 
   for (uint32_t i = threadIdx.x; i < BM + BN; i += 256)
     scales[i] = i < BM ? p.a.scales[m0 + min(i, m_last)] : bs[n0 + min(i - BM, n_last)];
 
-  i32x16 acc[FM][FN];
+  i32x4 acc[2 * FM][2 * FN];
 #pragma unroll
-  for (int i = 0; i < FM; i++)
+  for (int i = 0; i < 2 * FM; i++)
 #pragma unroll
-    for (int j = 0; j < FN; j++) acc[i][j] = i32x16{};
+    for (int j = 0; j < 2 * FN; j++) acc[i][j] = i32x4{};
+  if constexpr (FM * FN == 16) hold(acc);  // written before the barrier below
 
   load_all(st0, 0);
-  load_all(st1, 1);
-  load_all(st2, 2);
-  wait_and_meet<2 * kLoads>();
-  Fragments<FM, FN> f0, f1;
-  read(st0, at, 0, f0);
-  // Stage s is in `now`, its first fragments are in registers.  The last stages
-  // (`more` false) load nothing.
-  auto turn = [&](uint32_t s, auto more, const St& now, const St& next, St& free) {
-    read(now, at, 1, f1);
-    multiply<FM, FN>(f0, acc, [&](int i) {
-      if (more) load(free, s + 3, i);
-    });
-    if (more) wait_and_meet<2 * kLoads>();
-    else wait_and_meet<0>();
-    read(next, at, 0, f0);
-    multiply<FM, FN>(f1, acc, [](int) {});
-  };
-  constexpr std::true_type more;
-  constexpr std::false_type last;
-  for (uint32_t u = 0; u < fours; u++) {
-    turn(4 * u, more, st0, st1, st3);
-    turn(4 * u + 1, more, st1, st2, st0);
-    turn(4 * u + 2, more, st2, st3, st1);
-    turn(4 * u + 3, more, st3, st0, st2);
+  if constexpr (STAGES == 4) {
+    load_all(st1, 1);
+    load_all(st2, 2);
+    wait_and_meet<2 * kLoads>();
+  } else {
+    wait_and_meet<0>();
+    load_all(st1, 1);
   }
-  if (stages & 2) {  // stages are pairs: rows are padded to 128 codes
-    turn(4 * fours, last, st0, st1, st3);
-    turn(4 * fours + 1, last, st1, st2, st0);
+  // A step's fragments of b are read a step ahead, those of a as the multiplications
+  // free them: both twice would not fit the registers beside the sums.
+  i32x4 fa[2 * FM], b0[2 * FN], b1[2 * FN];
+  read_b(st0, at, 0, b0);
+#pragma unroll
+  for (int i = 0; i < 2 * FM; i++) fa[i] = read_a(st0, at, 0, i);
+  // Stage s is in `now`, its first fragments are in registers.  With two stages,
+  // the loads of stage s + 2 begin behind the barrier, into `now`, which all waves
+  // have read; with four, those of stage s + 3 go into the stage before.
+  auto turn = [&](uint32_t s, St& now, St& next, St& free) {
+    read_b(now, at, 1, b1);
+    multiply(fa, b0, acc, [&](int i) {
+      fa[i] = read_a(now, at, 1, i);
+      if (STAGES == 4) load(free, s + 3, i);
+    });
+    wait_and_meet<STAGES == 4 ? 2 * kLoads : 0>();
+    read_b(next, at, 0, b0);
+    multiply(fa, b1, acc, [&](int i) {
+      fa[i] = read_a(next, at, 0, i);
+      if (STAGES == 2) load(now, s + 2, i);
+    });
+  };
+  uint32_t s = 0;
+  if constexpr (STAGES == 4) {
+    for (; s + 4 <= stages; s += 4) {
+      turn(s, st0, st1, st3);
+      turn(s + 1, st1, st2, st0);
+      turn(s + 2, st2, st3, st1);
+      turn(s + 3, st3, st0, st2);
+    }
+    if (s < stages) turn(s, st0, st1, st3);
+    if (s + 1 < stages) turn(s + 1, st1, st2, st0);
+    if (s + 2 < stages) turn(s + 2, st2, st3, st1);
+  } else {
+    for (; s + 2 <= stages; s += 2) {
+      turn(s, st0, st1, st1);
+      turn(s + 1, st1, st0, st0);
+    }
+    if (s < stages) turn(s, st0, st1, st1);
   }
   wait_and_meet<0>();  // the stages' memory is used again below
+  if constexpr (FM * FN == 16) finished(acc);
 
-  // A lane has row lane & 31 of y and 4 consecutive columns in each quarter
-  // of a result: 32 rows at a time go through LDS (this wave's own part) and
-  // leave as whole 16-byte pieces.  Sums become floats, are scaled and rounded
-  // once, here.
+  // A lane has row lane & 15 of y and 4 consecutive columns of a result: 32 rows at
+  // a time go through LDS (this wave's own part) and leave as whole 16-byte pieces.
+  // Sums become floats, are scaled and rounded once, here.
   constexpr uint32_t kRow = 32 * FN * sizeof(T), kPitch = kRow + 16;
-  static_assert(32 * kPitch <= sizeof(St), "the stage holds the results");
-  uint8_t* out = reinterpret_cast<uint8_t*>(wave == 0   ? &st0
-                                             : wave == 1 ? &st1
-                                             : wave == 2 ? &st2
-                                                         : &st3);
+  static_assert(2 * 32 * kPitch <= sizeof(St), "a stage holds the results of two waves");
+  uint8_t* out = reinterpret_cast<uint8_t*>(wave & 1 ? &st1 : &st0) + (wave >> 1) * 32 * kPitch;
   const uint32_t nw = n0 + wn * 32 * FN;
 #pragma unroll
   for (int i = 0; i < FM; i++) {
-    const float sa = scales[wm * 32 * FM + i * 32 + r];
 #pragma unroll
-    for (int j = 0; j < FN; j++)
+    for (int h = 0; h < 2; h++) {
+      const float sa = scales[wm * 32 * FM + i * 32 + h * 16 + r];
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const uint32_t col = j * 32 + q * 8 + g * 4;
+      for (int j = 0; j < 2 * FN; j++) {
+        const uint32_t col = j * 16 + g * 4;
         float sb[4];
         __builtin_memcpy(sb, __builtin_assume_aligned(scales + BM + wn * 32 * FN + col, 16), 16);
         T v[4];
 #pragma unroll
-        for (int u = 0; u < 4; u++) v[u] = (T)in_fp32<T>((float)acc[i][j][4 * q + u] * sa * sb[u]);
-        __builtin_memcpy(out + r * kPitch + col * sizeof(T), v, sizeof(v));
+        for (int u = 0; u < 4; u++)
+          v[u] = (T)in_fp32<T>((float)acc[2 * i + h][j][u] * sa * sb[u]);
+        __builtin_memcpy(out + (h * 16 + r) * kPitch + col * sizeof(T), v, sizeof(v));
       }
+    }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     __builtin_amdgcn_wave_barrier();
     constexpr uint32_t kLanes = kRow / 16, kTogether = 64 / kLanes, kE = 16 / sizeof(T);
@@ -361,7 +407,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void i8_few(const Product p) {
 
 ec_status launched() { return hipGetLastError() == hipSuccess ? EC_OK : EC_ERR_DEVICE; }
 
-template <int FM, int FN, typename T, int MODE>
+template <int FM, int FN, int STAGES, typename T, int MODE>
 ec_status tiles_as(Product p, hipStream_t s) {
   p.n_tiles = (uint32_t)ceil_div(p.cols, 64 * FN);
   uint64_t m = ceil_div(p.rows, 64 * FM);
@@ -372,19 +418,77 @@ ec_status tiles_as(Product p, hipStream_t s) {
   p.m_tiles = (uint32_t)m;
   const uint64_t row = p.cols * sizeof(T), bytes = p.rows * row;
   if (FM > 1 && past_caches(bytes, row)) {
-    hipLaunchKernelGGL((i8_tiles<FM, FN, T, MODE, true>), grid_of(tiles), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((i8_tiles<FM, FN, STAGES, T, MODE, true>), grid_of(tiles), dim3(256), 0, s, p);
     return launched();
   }
-  hipLaunchKernelGGL((i8_tiles<FM, FN, T, MODE, false>), grid_of(tiles), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((i8_tiles<FM, FN, STAGES, T, MODE, false>), grid_of(tiles), dim3(256), 0, s, p);
   return launched();
 }
 
-// Rows and columns of a tile.
-uint32_t side_of(int mode, uint64_t rows, uint64_t cols, uint64_t groups) {
+// Which tile: by what a round of workgroups costs, in us times 1024: large ones
+// fill the 256 units one by one, of the others two share a unit.  Measured, us, as
+// tiles of 256, 128 and 64 (outputs, contraction, bf16):
+//   8192 x 8192, 512: 66, 58, 95; 4096 x 4096, 2048: 39, 41, 57; 8192: 105, 119, 187;
+//   2048 x 4096, 4096: 49, 33, 50; 1024 x 4096, 4096: 48, 21, 26; 500 x 4096, 4096:
+//   47, 19, 14; 200 x 8192, 8192: 82, 31, 26; 100 x 4096, 4096: 45, 17, 6.8.
+// Experts' weights are read anew by every group's tiles: 32768 rows, 64 experts,
+// 2048 outputs, contraction 4096: 349, 377, 529; 1024: 147, 134, 204; 2048 rows, 32
+// experts, 1024 outputs, 2048: 31, 27, 20.  Outputs in fp32 cost their stores: 8192 x
+// 8192, 512: 93, 76, 106.
+struct Tiles {
+  uint64_t large, small, least;  // how many of 256, 128 and 64
+  uint64_t cost[3];
+};
+Tiles tiles_for(int mode, uint64_t rows, uint64_t cols, uint64_t depth, uint64_t groups,
+                size_t bytes) {
   const uint64_t extra = mode == kExperts ? groups / 2 : 0;  // half a tile more for each
-  const uint64_t large = (ceil_div(rows, 256) + extra) * ceil_div(cols, 256);
-  const uint64_t small = (ceil_div(rows, 128) + extra) * ceil_div(cols, 128);
-  return large >= 192 ? 256 : small >= 128 ? 128 : 64;
+  auto tiles = [&](uint64_t side) { return (ceil_div(rows, side) + extra) * ceil_div(cols, side); };
+  const bool experts = mode == kExperts, wide = bytes == 4;
+  // a round of `at_once`, a last one that is at most half full as half of one
+  auto cost = [&](uint64_t n, uint64_t at_once, uint64_t start, uint64_t per8) {
+    const uint64_t halves = ceil_div(2 * n, at_once);
+    return (halves < 2 ? 2 : halves) * (start * 1024 + depth * per8 / 8) / 2;
+  };
+  Tiles t{tiles(256), tiles(128), tiles(64), {}};
+  t.cost[0] = ceil_div(t.large, 256) *
+              ((experts ? 16 : wide ? 18 : 12) * 1024 + depth * (experts ? 108 : 86) / 8);
+  t.cost[1] = t.small <= 256 ? cost(t.small, 256, experts ? 7 : 5, experts ? 48 : 32)
+                             : cost(t.small, 512, experts ? 6 : wide ? 7 : 5, experts ? 72 : 52);
+  t.cost[2] = t.least <= 256 ? cost(t.least, 256, 2, experts ? 16 : 10)
+                             : cost(t.least, 512, wide ? 3 : 2, experts ? 26 : 24);
+  return t;
+}
+// Rows and columns of a tile.
+uint32_t side_of(const Tiles& t) {
+  if (t.cost[0] <= t.cost[1] && t.cost[0] <= t.cost[2]) return 256;
+  return t.cost[1] <= t.cost[2] ? 128 : 64;
+}
+
+// Rows (a multiple of 256) that go first as large tiles where the rest would begin
+// another round, and costs less in a launch of its own: 4100 x 4096 x 4096 (rows,
+// contraction, columns) takes 80 us in one, as tiles of 128.
+uint64_t rows_first(uint64_t rows, uint64_t cols, uint64_t depth, size_t bytes) {
+  auto cost = [&](uint64_t n) {
+    if (n <= 16) return 3 * 1024 + (cols * depth >> 12);
+    const Tiles t = tiles_for(kDense, n, cols, depth, 1, bytes);
+    const uint64_t least = t.cost[1] < t.cost[2] ? t.cost[1] : t.cost[2];
+    return t.cost[0] < least ? t.cost[0] : least;
+  };
+  const uint64_t main = rows / 256 * 256;
+  if (main == 0 || main == rows) return 0;
+  const Tiles t = tiles_for(kDense, main, cols, depth, 1, bytes);
+  return t.cost[0] + 6 * 1024 + cost(rows - main) < cost(rows) ? main : 0;
+}
+
+template <typename T, int MODE>
+ec_status tiles_of(const Product& p, hipStream_t s) {
+  const Tiles t = tiles_for(MODE, p.rows, p.cols, p.depth, p.experts, sizeof(T));
+  switch (side_of(t)) {
+    case 256: return tiles_as<4, 4, 2, T, MODE>(p, s);
+    case 128:
+      return t.small <= 256 ? tiles_as<2, 2, 4, T, MODE>(p, s) : tiles_as<2, 2, 2, T, MODE>(p, s);
+    default: return tiles_as<1, 1, 4, T, MODE>(p, s);
+  }
 }
 
 // Whether the kernel for few rows runs.
@@ -407,18 +511,20 @@ ec_status product_as(Product p, hipStream_t s) {
     hipLaunchKernelGGL((i8_few<T>), grid_of(blocks), dim3(64 * waves), 0, s, p);
     return launched();
   }
-  const uint32_t side = side_of(p.experts ? kExperts : kDense, p.rows, p.cols, p.experts);
-  if (p.experts) {
-    if (side == 256) return tiles_as<4, 4, T, kExperts>(p, s);
-    if (side == 128) return tiles_as<2, 2, T, kExperts>(p, s);
-    return tiles_as<1, 1, T, kExperts>(p, s);
-  }
-  if (side == 256) return tiles_as<4, 4, T, kDense>(p, s);
-  if (side == 128) return tiles_as<2, 2, T, kDense>(p, s);
-  return tiles_as<1, 1, T, kDense>(p, s);
+  return p.experts ? tiles_of<T, kExperts>(p, s) : tiles_of<T, kDense>(p, s);
 }
 
-ec_status product(const Product& p, int type, hipStream_t s) {
+ec_status product(Product p, int type, hipStream_t s) {
+  const size_t bytes = type_bytes(type);
+  if (const uint64_t first = p.experts ? 0 : rows_first(p.rows, p.cols, p.depth, bytes)) {
+    Product rest = p;
+    rest.a = {p.a.codes + first * p.depth, p.a.scales + first};
+    rest.y = (uint8_t*)p.y + first * p.cols * bytes;
+    rest.rows = p.rows - first;
+    const ec_status st = product(rest, type, s);
+    if (st != EC_OK) return st;
+    p.rows = first;
+  }
   switch (type) {
     case EC_TYPE_F32: return product_as<float>(p, s);
     case EC_TYPE_F16: return product_as<f16_t>(p, s);
@@ -485,7 +591,8 @@ uint32_t ec_i8_product_tile(uint64_t rows, uint64_t cols, uint64_t depth, int ty
                             uint32_t experts) {
   if (!type_known(type) || rows == 0 || cols == 0 || depth == 0) return 0;
   if (few_rows(rows, experts)) return kFewRows;
-  return side_of(experts ? kExperts : kDense, rows, cols, experts);
+  return side_of(tiles_for(experts ? kExperts : kDense, rows, cols, depth, experts,
+                           type_bytes(type)));
 }
 
 size_t ec_i8_linear_workspace_bytes(uint64_t rows, uint64_t depth, uint64_t cols,

@@ -108,8 +108,8 @@ def test_product(rows, depth, cols, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 def test_product_of_the_largest_tiles(dtype):
-    rows, depth, cols = 3400, 390, 3700  # ragged tiles of 256 in both directions
-    assert ec.lib().ec_i8_product_tile(rows, cols, 512, 0, 0) == 256
+    rows, depth, cols = 3400, 4990, 3700  # ragged tiles of 256 in both directions
+    assert ec.lib().ec_i8_product_tile(rows, cols, 5120, 0, 0) == 256
     a, b = codes(1, rows, depth), codes(2, cols, depth)
     assert torch.equal(ec.i8_product(a, b, dtype), R.i8_product(a.codes, a.scales, b.codes, b.scales, dtype))
 
@@ -121,6 +121,13 @@ def test_sums_of_the_deepest_contraction_are_exact(rows):
     a.codes[0], b.codes[0], b.codes[1] = -128, -128, 127
     y = ec.i8_product(a, b, torch.float32)
     assert torch.equal(y, R.i8_product(a.codes, a.scales, b.codes, b.scales, torch.float32))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("rows", [4097, 4112, 4200, 4351])
+def test_rows_past_whole_tiles(rows, dtype):  # some in a launch of their own
+    a, b = codes(1, rows, 2000), codes(2, 4100, 2000)
+    assert torch.equal(ec.i8_product(a, b, dtype), R.i8_product(a.codes, a.scales, b.codes, b.scales, dtype))
 
 
 def split(rows, experts, seed, left=0):
