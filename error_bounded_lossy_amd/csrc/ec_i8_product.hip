@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "ec_i8.h"
+#include "ec_row_device.h"
 #include "ec_tile_device.h"
 
 using namespace ecmx;
@@ -319,49 +320,43 @@ __global__ __launch_bounds__(256, STAGES * FM * FN >= 16 ? 1 : 2) void i8_tiles(
 
 // ---------------------------------------------------------------- few rows
 
-// Up to 16 rows (of a group) against 16 columns a workgroup: what counts is
-// reading b once, at full bandwidth.  The waves divide the contraction in pieces
-// of 256 codes; a lane loads 16 bytes of a row of b and an instruction's 4 lanes
-// of a row 64 bytes, straight into registers, two pieces ahead.
+// Up to 16 rows against 16 columns a workgroup: what counts is reading b once, at
+// full bandwidth.  The waves divide the contraction in pieces of 256 codes; a lane
+// loads 16 bytes of a row of b and an instruction's 4 lanes of a row 64 bytes,
+// straight into registers, SETS pieces ahead: 4 where a wave has as many (1 x 8192 x
+// 8192: 15.8 us with 4, 17.1 with 2; 1 x 4096 x 4096: 6.6 and 6.4).
+//
+// With x unquantized (CHUNKS > 0), the workgroup quantizes its rows into LDS first,
+// while its first loads of b are in flight.
+//
+// (Rows of experts all go to the tiles, whose loads go past the registers: 128 rows
+// of 32 experts of 1024 x 2048 16.2 us there and 17.7 here, 512 rows 18.6 and 27.9.)
 constexpr uint32_t kFewCols = 16, kFewRows = 16, kFewWaves = 8, kPiece = 256;
-constexpr int kSteps = kPiece / 64, kSets = 2;
+constexpr int kSteps = kPiece / 64;
+// Elements that the workgroup quantizes: CHUNKS pieces of 8 a thread, 2 or 4, with
+// SETS = 2 where it is 4 (both do not fit 128 registers).
+constexpr uint32_t kFewElements = 4 * 8 * 64 * kFewWaves;
 
-template <typename T>
-__global__ __launch_bounds__(64 * kFewWaves, 4) void i8_few(const Product p) {
+struct Few {
+  Product p;
+  const void* x;
+  uint64_t stride;
+  uint32_t raw_depth;  // elements of a row of x
+};
+
+template <typename T, int CHUNKS, int SETS>  // CHUNKS = 0: x is in the 8-bit form
+__global__ __launch_bounds__(64 * kFewWaves, 4) void i8_few(const Few few) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t codes[];
   __shared__ __attribute__((aligned(16))) int part[kFewWaves][256];
+  __shared__ uint32_t tops[kFewRows];
+  const Product& p = few.p;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t waves = blockDim.x >> 6;
-  const uint32_t r = lane & 15, g = lane >> 4;
-  const uint32_t block = block_number(), tn = block % p.n_tiles;
-  const uint32_t n0 = tn * kFewCols;
-  uint64_t row0 = 0;
-  uint32_t here = (uint32_t)p.rows;
-  T* y = (T*)p.y;
-  const uint8_t* bc = p.b.codes;
-  const float* bs = p.b.scales;
-  if (p.experts) {
-    const GroupTile gt = find_tile(p.offsets, p.experts, p.rows, 4, block / p.n_tiles);
-    const uint64_t skip = (uint64_t)gt.local * kFewRows;
-    if (gt.group == p.experts) {  // rows of no group: zeros
-      const int64_t f = p.offsets[p.experts];
-      const uint64_t m0 = (f < 0 ? 0 : f) + skip, end = min(m0 + kFewRows, p.rows);
-      const uint32_t col = n0 + threadIdx.x % kFewCols;
-      if (col < p.cols)
-        for (uint64_t m = m0 + threadIdx.x / kFewCols; m < end; m += blockDim.x / kFewCols)
-          y[m * p.cols + col] = (T)0.0f;
-      return;
-    }
-    if (skip >= gt.count) return;  // only with offsets out of order
-    row0 = gt.first + skip;
-    here = (uint32_t)min((uint64_t)kFewRows, gt.count - skip);
-    bc += (uint64_t)gt.group * p.cols * p.depth;
-    bs += (uint64_t)gt.group * p.cols;
-  } else if (block >= p.n_tiles) {
-    return;
-  }
+  const uint32_t r = lane & 15, g = lane >> 4, rows = (uint32_t)p.rows;
+  const uint32_t block = block_number(), n0 = block * kFewCols;
+  if (block >= p.n_tiles) return;
   const uint32_t steps = p.depth / 64, pieces = (steps + kSteps - 1) / kSteps;
-  const uint8_t* gb = bc + (uint64_t)min(n0 + r, p.cols - 1) * p.depth + g * 16;
-  const uint8_t* ga = p.a.codes + (row0 + min(r, here - 1)) * p.depth + g * 16;
+  const uint8_t* gb = p.b.codes + (uint64_t)min(n0 + r, p.cols - 1) * p.depth + g * 16;
   struct Piece {
     i32x4 b[kSteps];
   };
@@ -370,14 +365,55 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void i8_few(const Product p) {
     for (int s = 0; s < kSteps; s++)  // steps past the end read the last one
       f.b[s] = *reinterpret_cast<const i32x4*>(gb + min(at * kSteps + s, steps - 1) * 64);
   };
-  Piece f[kSets];
+  Piece f[SETS];
 #pragma unroll
-  for (int i = 0; i < kSets; i++)
+  for (int i = 0; i < SETS; i++)
     if (wave + i * waves < pieces) load(f[i], wave + i * waves);
-  i32x4 acc = {};
-  for (uint32_t piece = wave; piece < pieces; piece += kSets * waves) {
+  const uint32_t lr = min(r, rows - 1);
+  const uint8_t* ga;
+  if constexpr (CHUNKS > 0) {
+    const uint32_t chunks = p.depth / 8, total = rows * chunks, pitch = p.depth + 16;
+    if (threadIdx.x < kFewRows) tops[threadIdx.x] = 0;
+    __syncthreads();
+    Eight<T> v[CHUNKS];
+    uint32_t row[CHUNKS], c[CHUNKS];
 #pragma unroll
-    for (int i = 0; i < kSets; i++) {
+    for (int q = 0; q < CHUNKS; q++) {
+      const uint32_t i = threadIdx.x + q * blockDim.x;
+      if (q * blockDim.x >= total) break;
+      row[q] = i / chunks, c[q] = i - row[q] * chunks;
+      v[q] = load_eight((const T*)few.x + row[q] * few.stride + c[q] * 8,
+                        i < total ? (int64_t)few.raw_depth - c[q] * 8 : 0);
+    }
+#pragma unroll
+    for (int q = 0; q < CHUNKS; q++) {
+      if (q * blockDim.x >= total) break;
+      float e[8];
+      widen(v[q], e);
+      // 16 lanes share a row
+      uint32_t m = max_of_8_lanes(magnitude_of_floats(e));
+      const uint32_t t = __builtin_amdgcn_mov_dpp(m, 0x140, 0xf, 0xf, true);
+      m = m > t ? m : t;
+      if (r == 0 && threadIdx.x + q * blockDim.x < total) atomicMax(&tops[row[q]], m);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < CHUNKS; q++) {
+      if (threadIdx.x + q * blockDim.x >= total) break;
+      float e[8];
+      widen(v[q], e);
+      *reinterpret_cast<uint2*>(codes + row[q] * pitch + c[q] * 8) =
+          code_row_eight(e, row_scale(tops[row[q]]).by);
+    }
+    __syncthreads();
+    ga = codes + lr * pitch + g * 16;
+  } else {
+    ga = p.a.codes + lr * p.depth + g * 16;
+  }
+  i32x4 acc = {};
+  for (uint32_t piece = wave; piece < pieces; piece += SETS * waves) {
+#pragma unroll
+    for (int i = 0; i < SETS; i++) {
       const uint32_t now = piece + i * waves;
       if (now >= pieces) break;
 #pragma unroll
@@ -388,18 +424,22 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void i8_few(const Product p) {
           acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(f[i].b[s], fa, acc, 0, 0, 0);
         }
       }
-      if (now + kSets * waves < pieces) load(f[i], now + kSets * waves);
+      if (now + SETS * waves < pieces) load(f[i], now + SETS * waves);
     }
   }
   // a lane has row r of y and columns 4 g .. 4 g + 3
   *reinterpret_cast<i32x4*>(&part[wave][r * 16 + g * 4]) = acc;
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < here * 16; i += blockDim.x) {
+  for (uint32_t i = threadIdx.x; i < rows * 16; i += blockDim.x) {
     int sum = 0;
     for (uint32_t w = 0; w < waves; w++) sum += part[w][i];
     const uint32_t col = n0 + i % 16;
-    const uint64_t row = row0 + i / 16;
-    if (col < p.cols) y[row * p.cols + col] = (T)in_fp32<T>((float)sum * p.a.scales[row] * bs[col]);
+    float scale;
+    if constexpr (CHUNKS > 0) scale = row_scale(tops[i / 16]).scale;
+    else scale = p.a.scales[i / 16];
+    if (col < p.cols)
+      ((T*)p.y)[(uint64_t)(i / 16) * p.cols + col] =
+          (T)in_fp32<T>((float)sum * scale * p.b.scales[col]);
   }
 }
 
@@ -491,26 +531,35 @@ ec_status tiles_of(const Product& p, hipStream_t s) {
   }
 }
 
-// Whether the kernel for few rows runs.
-bool few_rows(uint64_t rows, uint64_t experts) {
-  return (experts ? ceil_div(rows, experts) : rows) <= kFewRows;
+// Whether the kernel for few rows runs, and whether it quantizes the rows itself.
+bool few_rows(uint64_t rows, uint64_t experts) { return !experts && rows <= kFewRows; }
+bool few_quantizing(uint64_t rows, uint64_t padded, uint64_t experts) {
+  const uint64_t pieces = (padded + kPiece - 1) / kPiece;  // a short row has fewer waves
+  return few_rows(rows, experts) &&
+         rows * padded <= (pieces < kFewWaves ? pieces * 4 * 512 : kFewElements);
+}
+
+template <typename T, int CHUNKS, int SETS>
+ec_status few_sets(const Few& f, uint32_t waves, hipStream_t s) {
+  const uint32_t lds = CHUNKS ? (uint32_t)f.p.rows * (f.p.depth + 16) : 0;
+  hipLaunchKernelGGL((i8_few<T, CHUNKS, SETS>), grid_of(f.p.n_tiles), dim3(64 * waves), lds, s, f);
+  return launched();
+}
+template <typename T>
+ec_status few_of(Few f, bool quantize, hipStream_t s) {
+  f.p.n_tiles = (uint32_t)ceil_div(f.p.cols, kFewCols);
+  const uint32_t pieces = (f.p.depth + kPiece - 1) / kPiece;
+  const uint32_t waves = pieces < kFewWaves ? pieces : kFewWaves;
+  const uint64_t chunks = quantize ? ceil_div(f.p.rows * f.p.depth, 512 * waves) : 0;
+  if (chunks > 2) return few_sets<T, 4, 2>(f, waves, s);
+  const bool deep = pieces >= 4 * kFewWaves;
+  if (quantize) return deep ? few_sets<T, 2, 4>(f, waves, s) : few_sets<T, 2, 2>(f, waves, s);
+  return deep ? few_sets<T, 0, 4>(f, waves, s) : few_sets<T, 0, 2>(f, waves, s);
 }
 
 template <typename T>
-ec_status product_as(Product p, hipStream_t s) {
-  if (few_rows(p.rows, p.experts)) {
-    p.n_tiles = (uint32_t)ceil_div(p.cols, kFewCols);
-    // groups round up each, and the rows of no group once more
-    const uint64_t m = p.experts ? ceil_div(p.rows, kFewRows) +
-                                       (p.experts < p.rows ? p.experts : p.rows) + 1
-                                 : 1;
-    const uint64_t blocks = p.n_tiles * m;
-    if (blocks > kMostBlocks) return EC_ERR_UNSUPPORTED;
-    const uint32_t pieces = (p.depth + kPiece - 1) / kPiece;
-    const uint32_t waves = pieces < kFewWaves ? pieces : kFewWaves;
-    hipLaunchKernelGGL((i8_few<T>), grid_of(blocks), dim3(64 * waves), 0, s, p);
-    return launched();
-  }
+ec_status product_as(const Product& p, hipStream_t s) {
+  if (few_rows(p.rows, p.experts)) return few_of<T>(Few{p, nullptr, 0, 0}, false, s);
   return p.experts ? tiles_of<T, kExperts>(p, s) : tiles_of<T, kDense>(p, s);
 }
 
@@ -598,7 +647,7 @@ uint32_t ec_i8_product_tile(uint64_t rows, uint64_t cols, uint64_t depth, int ty
 size_t ec_i8_linear_workspace_bytes(uint64_t rows, uint64_t depth, uint64_t cols,
                                     uint32_t experts) {
   (void)cols;
-  (void)experts;
+  if (few_quantizing(rows, ec_mx_padded(depth), experts)) return 0;
   return code_bytes(rows, depth) + rows * 4;
 }
 
@@ -618,12 +667,23 @@ ec_status ec_i8_linear(const void* x, int type, uint64_t rows, uint64_t depth, u
   const size_t need = ec_i8_linear_workspace_bytes(rows, depth, cols, experts);
   if (need && !workspace) return EC_ERR_INVALID;
   if (workspace_bytes < need) return EC_ERR_CAPACITY;
+  const uint64_t padded = ec_mx_padded(depth);
+  if (few_quantizing(rows, padded, experts)) {
+    const Few f{product_of(nullptr, nullptr, rows, w_codes, w_scales, cols, padded, nullptr, 0, y),
+                x, stride, (uint32_t)depth};
+    hipStream_t s = (hipStream_t)stream;
+    switch (type) {
+      case EC_TYPE_F32: return few_of<float>(f, true, s);
+      case EC_TYPE_F16: return few_of<f16_t>(f, true, s);
+      default: return few_of<bf16_t>(f, true, s);
+    }
+  }
   uint8_t* codes = (uint8_t*)workspace;
   void* scales = codes + code_bytes(rows, depth);
   const ec_status st = ec_i8_quantize(x, type, rows, depth, stride, codes, scales, stream);
   if (st != EC_OK) return st;
-  return product(product_of(codes, scales, rows, w_codes, w_scales, cols, ec_mx_padded(depth),
-                            offsets, experts, y),
+  return product(product_of(codes, scales, rows, w_codes, w_scales, cols, padded, offsets, experts,
+                            y),
                  type, (hipStream_t)stream);
 }
 
