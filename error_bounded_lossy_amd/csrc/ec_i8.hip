@@ -10,10 +10,10 @@ namespace {
 // A row stays in registers between its magnitude and its codes (up to 16384
 // elements; longer rows are read twice).
 template <typename T, int PIECES>
-__global__ __launch_bounds__(kRowThreads) void i8_rows(const T* __restrict__ x, RowShape s,
+__global__ __launch_bounds__(kMostThreads) void i8_rows(const T* __restrict__ x, RowShape s,
                                                        uint64_t stride, uint8_t* codes,
                                                        float* scales) {
-  __shared__ uint32_t part[kRowWaves];
+  __shared__ uint32_t part[kMostWaves];
   const RowAt a = row_at(s, block_number());
   const bool here = a.row < s.rows;
   const T* from = x + (here ? a.row : s.rows - 1) * stride;
@@ -47,14 +47,14 @@ __global__ __launch_bounds__(kRowThreads) void i8_rows(const T* __restrict__ x, 
       float f[8];
       widen(v[i], f);
       if (c < s.chunks)
-        *reinterpret_cast<uint2*>(to + (uint64_t)c * 8) = code_row_eight(f, r.by);
+        *reinterpret_cast<uint2*>(to + (uint64_t)c * 8) = code_row_eight(f, r);
     }
   }
   if (a.lane == 0) scales[a.row] = r.scale;
 }
 
 template <typename T>
-__global__ __launch_bounds__(kRowThreads) void i8_values(const uint8_t* __restrict__ codes,
+__global__ __launch_bounds__(kMostThreads) void i8_values(const uint8_t* __restrict__ codes,
                                                          const float* __restrict__ scales,
                                                          RowShape s, uint64_t padded, T* y,
                                                          uint64_t stride) {
@@ -74,22 +74,28 @@ __global__ __launch_bounds__(kRowThreads) void i8_values(const uint8_t* __restri
 
 // ---------------------------------------------------------------- host
 
+// Under as many rows, each has as many lanes as it can: what counts is when the
+// last lane is done.
+constexpr uint64_t kFewRows = 64;
+
 ec_status launched() { return hipGetLastError() == hipSuccess ? EC_OK : EC_ERR_DEVICE; }
 
 template <typename T>
 ec_status rows_of(const void* x, uint64_t rows, uint64_t cols, uint64_t stride, void* codes,
                   void* scales, hipStream_t stream) {
-  uint32_t pieces;
-  const RowShape s = row_shape(rows, cols, ec_mx_padded(cols) / 8, pieces);
+  uint32_t pieces, threads;
+  const bool few = rows < kFewRows;
+  const RowShape s =
+      row_shape(rows, cols, ec_mx_padded(cols) / 8, few ? 1 : 2, few ? 1 : 2, 64, pieces, threads);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid_of(row_blocks(s)), dim3(kRowThreads), 0, stream, (const T*)x,
-                       s, stride, (uint8_t*)codes, (float*)scales);
+    hipLaunchKernelGGL(kernel, grid_of(row_blocks(s, threads)), dim3(threads), 0, stream,
+                       (const T*)x, s, stride, (uint8_t*)codes, (float*)scales);
   };
   switch (pieces) {
     case 1: go(i8_rows<T, 1>); break;
     case 2: go(i8_rows<T, 2>); break;
-    case 4: go(i8_rows<T, 4>); break;
-    default: go(i8_rows<T, 8>);
+    case 3: go(i8_rows<T, 3>); break;
+    default: go(i8_rows<T, 4>);
   }
   return launched();
 }
@@ -97,9 +103,10 @@ ec_status rows_of(const void* x, uint64_t rows, uint64_t cols, uint64_t stride, 
 template <typename T>
 ec_status values_of(const void* codes, const void* scales, uint64_t rows, uint64_t cols, void* y,
                     uint64_t stride, hipStream_t stream) {
-  uint32_t pieces;
-  const RowShape s = row_shape(rows, cols, ceil_div(cols, 8), pieces);
-  hipLaunchKernelGGL((i8_values<T>), grid_of(row_blocks(s)), dim3(kRowThreads), 0, stream,
+  uint32_t pieces, threads;
+  const bool few = rows < kFewRows;
+  const RowShape s = row_shape(rows, cols, ceil_div(cols, 8), few ? 1 : 2, few ? 1 : 2, 64, pieces, threads);
+  hipLaunchKernelGGL((i8_values<T>), grid_of(row_blocks(s, threads)), dim3(threads), 0, stream,
                      (const uint8_t*)codes, (const float*)scales, s, ec_mx_padded(cols), (T*)y,
                      stride);
   return launched();

@@ -403,7 +403,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void i8_few(const Few few) {
       float e[8];
       widen(v[q], e);
       *reinterpret_cast<uint2*>(codes + row[q] * pitch + c[q] * 8) =
-          code_row_eight(e, row_scale(tops[row[q]]).by);
+          code_row_eight(e, row_scale(tops[row[q]]));
     }
     __syncthreads();
     ga = codes + lr * pitch + g * 16;

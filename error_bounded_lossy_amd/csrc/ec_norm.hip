@@ -10,7 +10,7 @@ using namespace ecmx;
 
 namespace {
 
-// Eight weights from element c on; those past the row's end are not used.
+// Eight weights from element c on; those past the row's end are zero.
 __device__ __forceinline__ void weights_at(const void* w, int type, uint64_t c, int64_t n,
                                            float (&f)[8]) {
   if (type == EC_TYPE_F32) widen(load_eight((const float*)w + c, n), f);
@@ -29,43 +29,57 @@ struct Norm {
 };
 
 // One pass over x and the residual: the row stays in registers (up to 16384
-// elements; longer rows are read again from h, or x, in each pass).
+// elements; longer rows are read again from h, or x, in each pass).  The weights
+// are asked for before the sum is known.
 template <typename T, int PIECES, bool EIGHT_BITS>
-__global__ __launch_bounds__(kRowThreads) void rms_norm(const Norm p, RowShape s) {
-  __shared__ float sums[kRowWaves];
-  __shared__ uint32_t tops[kRowWaves];
+__global__ __launch_bounds__(kMostThreads) void rms_norm(const Norm p, RowShape s) {
+  __shared__ float sums[kMostWaves];
+  __shared__ uint32_t tops[kMostWaves];
   const RowAt a = row_at(s, block_number());
   const bool here = a.row < s.rows;
   const uint64_t row = here ? a.row : s.rows - 1;
   const T* x = (const T*)p.x + row * p.stride;
   const T* residual = p.residual ? (const T*)p.residual + row * p.residual_stride : nullptr;
   T* h = p.h ? (T*)p.h + row * s.cols : nullptr;
+  auto chunk = [&](uint32_t round, int i) { return (round * PIECES + i) * a.lanes + a.lane; };
+  auto left = [&](uint32_t c) { return (int64_t)s.cols - (int64_t)c * 8; };
   Eight<T> v[PIECES];
+  float w[PIECES][8];
+  auto load_weights = [&](uint32_t round) {
+#pragma unroll
+    for (int i = 0; i < PIECES; i++) {
+      const uint32_t c = chunk(round, i);
+      weights_at(p.weight, p.wtype, (uint64_t)c * 8, left(c), w[i]);
+    }
+  };
   float sum = 0;
   for (uint32_t round = 0; round < s.rounds; round++) {
 #pragma unroll
     for (int i = 0; i < PIECES; i++) {
-      const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
-      v[i] = load_eight(x + (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8);
+      const uint32_t c = chunk(round, i);
+      v[i] = load_eight(x + (uint64_t)c * 8, left(c));
     }
     if (residual) {
       Eight<T> r[PIECES];
 #pragma unroll
       for (int i = 0; i < PIECES; i++) {
-        const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
-        r[i] = load_eight(residual + (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8);
+        const uint32_t c = chunk(round, i);
+        r[i] = load_eight(residual + (uint64_t)c * 8, left(c));
       }
+      if (s.rounds == 1) load_weights(0);
 #pragma unroll
       for (int i = 0; i < PIECES; i++) {
-        const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
+        const uint32_t c = chunk(round, i);
         float f[8], g[8];
         widen(v[i], f);
         widen(r[i], g);
 #pragma unroll
         for (int j = 0; j < 8; j++) f[j] += g[j];
         v[i] = narrow<T>(f);
-        if (here) store_eight(h + (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8, v[i]);
+        if (here) store_eight(h + (uint64_t)c * 8, left(c), v[i]);
       }
+    } else if (s.rounds == 1) {
+      load_weights(0);
     }
 #pragma unroll
     for (int i = 0; i < PIECES; i++) {
@@ -80,35 +94,37 @@ __global__ __launch_bounds__(kRowThreads) void rms_norm(const Norm p, RowShape s
   if (here && p.rstd && a.lane == 0) p.rstd[row] = rstd;
   const T* again = residual ? h : x;
   auto normed = [&](uint32_t round, int i, float (&f)[8]) {
-    const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
-    const int64_t n = (int64_t)s.cols - (int64_t)c * 8;
-    float w[8];
-    weights_at(p.weight, p.wtype, (uint64_t)c * 8, n, w);
-    if (s.rounds > 1) v[i] = load_eight(again + (uint64_t)c * 8, n);
+    const uint32_t c = chunk(round, i);
+    if (s.rounds > 1) {
+      weights_at(p.weight, p.wtype, (uint64_t)c * 8, left(c), w[i]);
+      v[i] = load_eight(again + (uint64_t)c * 8, left(c));
+    }
     widen(v[i], f);
 #pragma unroll
-    for (int j = 0; j < 8; j++) f[j] = f[j] * rstd * w[j];
+    for (int j = 0; j < 8; j++) f[j] = f[j] * rstd * w[i][j];
   };
   if constexpr (!EIGHT_BITS) {
     T* y = (T*)p.y + row * s.cols;
     for (uint32_t round = 0; round < s.rounds; round++)
 #pragma unroll
       for (int i = 0; i < PIECES; i++) {
-        const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
+        const uint32_t c = chunk(round, i);
         float f[8];
         normed(round, i, f);
-        if (here)
-          store_eight(y + (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8, narrow<T>(f));
+        if (here) store_eight(y + (uint64_t)c * 8, left(c), narrow<T>(f));
       }
   } else {
     uint32_t m = 0;
-    float f[PIECES][8];
     for (uint32_t round = 0; round < s.rounds; round++)
 #pragma unroll
       for (int i = 0; i < PIECES; i++) {
-        normed(round, i, f[i]);
-        const uint32_t n = magnitude_of_floats(f[i]);
+        float f[8];
+        normed(round, i, f);
+        const uint32_t n = magnitude_of_floats(f);
         m = m > n ? m : n;
+        if (s.rounds == 1)  // the products take the weights' place
+#pragma unroll
+          for (int j = 0; j < 8; j++) w[i][j] = f[j];
       }
     const RowScale r = row_scale(max_over_row(m, s.shift, tops));
     if (!here) return;
@@ -116,10 +132,12 @@ __global__ __launch_bounds__(kRowThreads) void rms_norm(const Norm p, RowShape s
     for (uint32_t round = 0; round < s.rounds; round++)
 #pragma unroll
       for (int i = 0; i < PIECES; i++) {
-        const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
-        if (s.rounds > 1) normed(round, i, f[i]);
+        const uint32_t c = chunk(round, i);
+        float f[8];
+        if (s.rounds > 1) normed(round, i, f);
         if (c < s.chunks)
-          *reinterpret_cast<uint2*>(codes + (uint64_t)c * 8) = code_row_eight(f[i], r.by);
+          *reinterpret_cast<uint2*>(codes + (uint64_t)c * 8) =
+              code_row_eight(s.rounds > 1 ? f : w[i], r);
       }
     if (a.lane == 0) p.scales[row] = r.scale;
   }
@@ -136,81 +154,112 @@ struct Back {
 };
 
 // A workgroup takes every gridDim-th set of rows and adds up what they give to
-// dweight in registers.
+// dweight in registers; the next set's rows are on their way while it works on one.
 template <typename T, int PIECES>
-__global__ __launch_bounds__(kRowThreads) void rms_norm_back(const Back p, RowShape s) {
-  __shared__ float sums[2][kRowWaves];
-  const uint32_t slots = kRowThreads >> s.shift;
-  const uint64_t sets = (s.rows + slots - 1) / slots;
-  float dw[PIECES][8] = {};
+__global__ __launch_bounds__(kMostThreads) void rms_norm_back(const Back p, RowShape s) {
+  __shared__ float sums[2][kMostWaves];
+  // (of four pieces the registers hold one row: 2000 x 16384 bf16 72 us, else over 150)
+  constexpr bool kAhead = PIECES <= 3;
+  const uint64_t sets = (s.rows + row_slots(s.shift) - 1) / row_slots(s.shift);
+  struct Row {
+    Eight<T> dy[PIECES], h[PIECES], dh[PIECES];
+    float rstd;
+  };
+  auto chunk = [&](const RowAt& a, uint32_t round, int i) {
+    return (round * PIECES + i) * a.lanes + a.lane;
+  };
+  auto left = [&](uint32_t c) { return (int64_t)s.cols - (int64_t)c * 8; };
+  auto load = [&](uint64_t set, uint32_t round, Row& r) {
+    const RowAt a = row_at(s, set);
+    const bool here = a.row < s.rows;
+    const uint64_t row = here ? a.row : s.rows - 1;
+    r.rstd = p.rstd[row];
+#pragma unroll
+    for (int i = 0; i < PIECES; i++) {
+      const uint32_t c = chunk(a, round, i);
+      const uint64_t at = row * s.cols + (uint64_t)c * 8;
+      const int64_t n = here ? left(c) : 0;
+      r.dy[i] = load_eight((const T*)p.dy + at, n);
+      r.h[i] = load_eight((const T*)p.h + at, n);
+      if (p.dh) r.dh[i] = load_eight((const T*)p.dh + at, n);
+    }
+  };
+  float w[PIECES][8], dw[PIECES][8] = {};
+  auto load_weights = [&](uint32_t round) {
+    const RowAt a = row_at(s, 0);
+#pragma unroll
+    for (int i = 0; i < PIECES; i++) {
+      const uint32_t c = chunk(a, round, i);
+      weights_at(p.weight, p.wtype, (uint64_t)c * 8, left(c), w[i]);
+    }
+  };
+  Row now, next;
+  if (s.rounds == 1) load_weights(0);
+  load(blockIdx.x, 0, now);
   uint32_t turn = 0;
   for (uint64_t set = blockIdx.x; set < sets; set += gridDim.x, turn ^= 1) {
     const RowAt a = row_at(s, set);
-    const bool here = a.row < s.rows;
-    const uint64_t at = (here ? a.row : s.rows - 1) * s.cols;
-    const float rstd = p.rstd[here ? a.row : s.rows - 1];
-    const T *dy = (const T*)p.dy + at, *h = (const T*)p.h + at;
-    Eight<T> d[PIECES], v[PIECES];
-    auto load = [&](uint32_t round) {
-#pragma unroll
-      for (int i = 0; i < PIECES; i++) {
-        const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
-        const int64_t n = here ? (int64_t)s.cols - (int64_t)c * 8 : 0;
-        d[i] = load_eight(dy + (uint64_t)c * 8, n);
-        v[i] = load_eight(h + (uint64_t)c * 8, n);
-      }
-    };
+    const bool more = set + gridDim.x < sets;
     float dot = 0;
     for (uint32_t round = 0; round < s.rounds; round++) {
-      load(round);
+      if (s.rounds > 1) {
+        load(set, round, now);
+        load_weights(round);
+      } else if (kAhead && more) {
+        load(set + gridDim.x, 0, next);
+      }
 #pragma unroll
       for (int i = 0; i < PIECES; i++) {
-        const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
-        float f[8], g[8], w[8];
-        widen(d[i], f);
-        widen(v[i], g);
-        weights_at(p.weight, p.wtype, (uint64_t)c * 8, (int64_t)s.cols - (int64_t)c * 8, w);
+        float f[8], g[8];
+        widen(now.dy[i], f);
+        widen(now.h[i], g);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-          const float n = g[j] * rstd;
-          dot += f[j] * w[j] * n;
+          const float n = g[j] * now.rstd;
+          dot += f[j] * w[i][j] * n;
           dw[i][j] += f[j] * n;
         }
       }
     }
     // two sets of words in turn: a wave may be one row ahead of another
     dot = sum_over_row(dot, s.shift, sums[turn]) / (float)s.cols;
-    if (here)
+    if (a.row < s.rows)
       for (uint32_t round = 0; round < s.rounds; round++) {
-        if (s.rounds > 1) load(round);
+        if (s.rounds > 1) {
+          load(set, round, now);
+          load_weights(round);
+        }
 #pragma unroll
         for (int i = 0; i < PIECES; i++) {
-          const uint32_t c = (round * PIECES + i) * a.lanes + a.lane;
-          const int64_t n = (int64_t)s.cols - (int64_t)c * 8;
-          float f[8], g[8], w[8], o[8] = {};
-          widen(d[i], f);
-          widen(v[i], g);
-          weights_at(p.weight, p.wtype, (uint64_t)c * 8, n, w);
-          if (p.dh) widen(load_eight((const T*)p.dh + at + (uint64_t)c * 8, n), o);
+          const uint32_t c = chunk(a, round, i);
+          float f[8], g[8], o[8] = {};
+          widen(now.dy[i], f);
+          widen(now.h[i], g);
+          if (p.dh) widen(now.dh[i], o);
 #pragma unroll
-          for (int j = 0; j < 8; j++) o[j] += rstd * (f[j] * w[j] - g[j] * rstd * dot);
-          store_eight((T*)p.dx + at + (uint64_t)c * 8, n, narrow<T>(o));
+          for (int j = 0; j < 8; j++)
+            o[j] += now.rstd * (f[j] * w[i][j] - g[j] * now.rstd * dot);
+          store_eight((T*)p.dx + a.row * s.cols + (uint64_t)c * 8, left(c), narrow<T>(o));
         }
       }
+    if (s.rounds == 1 && more) {
+      if (kAhead) now = next;
+      else load(set + gridDim.x, 0, now);
+    }
   }
   if (!p.parts) return;
-  const uint32_t lanes = 1u << s.shift, lane = threadIdx.x & (lanes - 1);
-  float* to = p.parts + ((uint64_t)blockIdx.x * slots + (threadIdx.x >> s.shift)) * s.cols;
+  const RowAt a = row_at(s, blockIdx.x);
+  float* to = p.parts + a.row * s.cols;
 #pragma unroll
   for (int i = 0; i < PIECES; i++) {
-    const uint64_t c = (uint64_t)(i * lanes + lane) * 8;
+    const uint64_t c = (uint64_t)chunk(a, 0, i) * 8;
 #pragma unroll
     for (int j = 0; j < 8; j++)
       if (c + j < s.cols) to[c + j] = dw[i][j];
   }
 }
 
-constexpr uint32_t kSumCols = 32, kSumSlices = 32;
+constexpr uint32_t kSumCols = 32, kSumSlices = 32, kSumAhead = 8;
 
 // Column sums of [parts][cols]: 32 columns a workgroup, their rows in 32 slices
 // that are joined in order.
@@ -239,7 +288,16 @@ __global__ __launch_bounds__(kSumCols* kSumSlices) void column_sums(const F from
   const uint64_t c = (uint64_t)blockIdx.x * kSumCols + col;
   float sum = 0;
   if (c < from.cols)
-    for (uint64_t r = slice; r < from.rows; r += kSumSlices) sum += from.at(r, (uint32_t)c);
+    for (uint64_t r0 = slice; r0 < from.rows; r0 += kSumSlices * kSumAhead) {
+      float v[kSumAhead];
+#pragma unroll
+      for (int i = 0; i < (int)kSumAhead; i++) {
+        const uint64_t r = r0 + i * kSumSlices;
+        v[i] = r < from.rows ? from.at(r, (uint32_t)c) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < (int)kSumAhead; i++) sum += v[i];
+    }
   part[slice][col] = sum;
   __syncthreads();
   if (slice || c >= from.cols) return;
@@ -275,19 +333,24 @@ ec_status check_norm(const Norm& p, int type, uint64_t rows, uint64_t cols) {
              : EC_ERR_INVALID;
 }
 
+// Under as many rows, each has as many lanes as it can: what counts is when the
+// last lane is done.
+constexpr uint64_t kFewRows = 64;
+
 template <typename T, bool EIGHT_BITS>
 ec_status norm_as(const Norm& p, uint64_t rows, uint64_t cols, hipStream_t stream) {
-  uint32_t pieces;
-  const RowShape s =
-      row_shape(rows, cols, EIGHT_BITS ? ec_mx_padded(cols) / 8 : ceil_div(cols, 8), pieces);
+  uint32_t pieces, threads;
+  const bool few = rows < kFewRows;
+  const RowShape s = row_shape(rows, cols, EIGHT_BITS ? ec_mx_padded(cols) / 8 : ceil_div(cols, 8),
+                               few ? 1 : 2, few ? 1 : 2, 64, pieces, threads);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid_of(row_blocks(s)), dim3(kRowThreads), 0, stream, p, s);
+    hipLaunchKernelGGL(kernel, grid_of(row_blocks(s, threads)), dim3(threads), 0, stream, p, s);
   };
   switch (pieces) {
     case 1: go(rms_norm<T, 1, EIGHT_BITS>); break;
     case 2: go(rms_norm<T, 2, EIGHT_BITS>); break;
-    case 4: go(rms_norm<T, 4, EIGHT_BITS>); break;
-    default: go(rms_norm<T, 8, EIGHT_BITS>);
+    case 3: go(rms_norm<T, 3, EIGHT_BITS>); break;
+    default: go(rms_norm<T, 4, EIGHT_BITS>);
   }
   return launched();
 }
@@ -300,32 +363,43 @@ ec_status norm(const Norm& p, int type, uint64_t rows, uint64_t cols, hipStream_
   }
 }
 
-// Workgroups of the backward pass: two rows a slot at least, so that dweight's
-// parts stay below half of dy's elements.
-uint32_t back_blocks(const RowShape& s) {
-  const uint64_t sets = ceil_div(s.rows, kRowThreads >> s.shift), n = ceil_div(sets, 2);
-  return (uint32_t)(n > 1024 ? 1024 : n);
+// Whole workgroups of 256 or 512 threads (a unit holds two of 256: one of 320 leaves
+// it half empty), with two pieces a lane where that makes a row: two rows and
+// dweight's sums fit its registers.
+RowShape back_shape(uint64_t rows, uint64_t cols, uint32_t& pieces, uint32_t& threads) {
+  return row_shape(rows, cols, ceil_div(cols, 8), 2, 3, kRowThreads, pieces, threads);
+}
+uint32_t slots_of(const RowShape& s, uint32_t threads) {
+  return s.shift == kWhole ? 1 : threads >> s.shift;
+}
+// Workgroups of the backward pass: as many as the units hold at a time, and two rows
+// a slot at least, so that dweight's parts stay below half of dy's elements.
+uint32_t back_blocks(const RowShape& s, uint32_t threads) {
+  const uint64_t n = ceil_div(row_blocks(s, threads), 2), most = 512 * kRowThreads / threads;
+  return (uint32_t)(n > most ? most : n);
 }
 
 template <typename T>
 ec_status back_as(Back p, uint64_t rows, uint64_t cols, void* dweight, void* workspace,
                   hipStream_t stream) {
-  uint32_t pieces;
-  const RowShape s = row_shape(rows, cols, ceil_div(cols, 8), pieces);
+  uint32_t pieces, threads;
+  const RowShape s = back_shape(rows, cols, pieces, threads);
   p.parts = s.rounds == 1 ? (float*)workspace : nullptr;
-  const uint32_t blocks = back_blocks(s);
+  const uint32_t blocks = back_blocks(s, threads);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kRowThreads), 0, stream, p, s);
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(threads), 0, stream, p, s);
   };
-  if (rows) switch (pieces) {
+  if (rows) {
+    switch (pieces) {
       case 1: go(rms_norm_back<T, 1>); break;
       case 2: go(rms_norm_back<T, 2>); break;
-      case 4: go(rms_norm_back<T, 4>); break;
-      default: go(rms_norm_back<T, 8>);
+      case 3: go(rms_norm_back<T, 3>); break;
+      default: go(rms_norm_back<T, 4>);
     }
+  }
   const dim3 grid((uint32_t)ceil_div(cols, kSumCols)), block(kSumCols * kSumSlices);
   if (p.parts || !rows) {
-    const PartRows f{p.parts, rows ? blocks * (uint64_t)(kRowThreads >> s.shift) : 0, s.cols};
+    const PartRows f{p.parts, rows ? blocks * (uint64_t)slots_of(s, threads) : 0, s.cols};
     hipLaunchKernelGGL((column_sums<PartRows>), grid, block, 0, stream, f, dweight, p.wtype);
   } else {
     const GradientRows<T> f{(const T*)p.dy, (const T*)p.h, p.rstd, rows, s.cols};
@@ -364,9 +438,9 @@ ec_status ec_rms_norm_i8(const void* x, uint64_t stride, const void* residual,
 
 size_t ec_rms_norm_backward_workspace_bytes(uint64_t rows, uint64_t cols) {
   if (rows == 0 || cols == 0) return 0;
-  uint32_t pieces;
-  const RowShape s = row_shape(rows, cols, ceil_div(cols, 8), pieces);
-  return s.rounds > 1 ? 0 : (size_t)back_blocks(s) * (kRowThreads >> s.shift) * cols * 4;
+  uint32_t pieces, threads;
+  const RowShape s = back_shape(rows, cols, pieces, threads);
+  return s.rounds > 1 ? 0 : (size_t)back_blocks(s, threads) * slots_of(s, threads) * cols * 4;
 }
 
 ec_status ec_rms_norm_backward(const void* dy, const void* h, const void* dh, int type,
