@@ -77,9 +77,10 @@ def expert_route(logits: torch.Tensor, choices: int, score: str = "softmax",
     if bias is not None:
         if bias.dtype != torch.float32 or bias.shape != (experts,) or bias.device != r.device:
             _refuse("expert_route: a float32 bias [experts] on the logits' device is wanted")
-        bias = bias.contiguous()
-    ids = torch.empty((tokens, choices), dtype=torch.int32, device=r.device)
-    weights = torch.empty((tokens, choices), dtype=torch.float32, device=r.device)
+        if not bias.is_contiguous():
+            bias = bias.contiguous()
+    ids = r.new_empty((tokens, choices), dtype=torch.int32)
+    weights = r.new_empty((tokens, choices), dtype=torch.float32)
     _b.check(_b.lib().ec_expert_route(
         r.data_ptr(), kind, tokens, stride, experts, None if bias is None else bias.data_ptr(),
         choices, SCORES[score], groups, top_groups, bool(renormalize), scale, ids.data_ptr(),
@@ -98,13 +99,14 @@ def expert_route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: tor
                             (dweights, logits, ids, score, renormalize, scale), stream)
     r, stride, kind = _logits(logits, score, scale, "expert_route_backward")
     tokens, experts = r.shape
-    if (not _ints(ids, (tokens, *ids.shape[1:])) or ids.dim() != 2 or ids.shape[1] == 0
+    if (ids.dim() != 2 or not _ints(ids, (tokens, ids.shape[1])) or ids.shape[1] == 0
             or dweights.dtype != torch.float32 or dweights.shape != ids.shape
-            or not ids.device == dweights.device == r.device):
+            or ids.device != r.device or dweights.device != r.device):
         _refuse("expert_route_backward: int32 ids and float32 dweights [tokens, choices] on the "
                 "logits' device are wanted")
-    dweights = dweights.contiguous()
-    dlogits = torch.empty((tokens, experts), dtype=r.dtype, device=r.device)
+    if not dweights.is_contiguous():
+        dweights = dweights.contiguous()
+    dlogits = r.new_empty((tokens, experts))
     _b.check(_b.lib().ec_expert_route_backward(
         dweights.data_ptr(), r.data_ptr(), kind, tokens, stride, experts, ids.data_ptr(),
         ids.shape[1], SCORES[score], bool(renormalize), scale, dlogits.data_ptr(),
@@ -195,16 +197,16 @@ def expert_dispatch_mx(x: torch.Tensor, routing: Routing, stream=None) -> MXTens
 
 def expert_dispatch_i8(x: I8Tensor, routing: Routing, stream=None) -> I8Tensor:
     """The same of tokens that are in the 8-bit form, as rms_norm_i8 makes them: x [tokens, cols]."""
-    if stream is not None or _b.elsewhere(x.codes):
+    if stream is not None or _b.elsewhere(x.home):
         return _b.on_stream(expert_dispatch_i8, (x, routing), stream)
     r = routing
-    if (len(x.lead) != 1 or x.lead[0] != r.tokens or x.cols == 0 or not x.codes.is_cuda
-            or x.codes.device != r.place.device):
+    if (len(x.lead) != 1 or x.lead[0] != r.tokens or x.cols == 0 or not x.home.is_cuda
+            or x.home.device != r.place.device):
         _refuse("expert_dispatch_i8: rows [tokens, cols] on the routing's device are wanted")
-    q = _empty_i8((r.tokens * r.choices,), x.cols, x.codes)
+    q = _empty_i8((r.tokens * r.choices,), x.cols, x.home)
     _b.check(_b.lib().ec_expert_dispatch_i8(
         *x.pointers(), r.tokens, x.padded, r.place.data_ptr(), r.choices, r.offsets.data_ptr(),
-        r.experts, *q.pointers(), _b.current_stream(x.codes)), "ec_expert_dispatch_i8")
+        r.experts, *q.pointers(), _b.current_stream(x.home)), "ec_expert_dispatch_i8")
     return q
 
 

@@ -19,29 +19,48 @@ class I8Tensor:
     """A tensor in the 8-bit form along its last dimension, of `cols` elements: codes, int8
     [..., padded] with zeros from cols on, and scales, float32 [...]."""
 
-    __slots__ = ("codes", "scales", "cols", "padded", "lead")
+    # What the library makes holds both in one allocation, `home`, codes first (`_scales` is None,
+    # and `_split` the bytes of codes), and has them as tensors only when asked, as an MXTensor
+    # does.  Addresses are taken at each call.
+    __slots__ = ("cols", "padded", "lead", "home", "_scales", "_split")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
         p = (cols + 127) // 128 * 128
+        *lead, width = form = codes.shape
         if (codes.dtype != torch.int8 or scales.dtype != torch.float32 or cols < 0
-                or codes.dim() == 0 or codes.shape[-1] != p or scales.shape != codes.shape[:-1]
+                or width != p or list(scales.shape) != lead
                 or not codes.is_contiguous() or not scales.is_contiguous()
                 or codes.device != scales.device):
             _refuse("I8Tensor: int8 codes [..., padded] and float32 scales [...], contiguous and "
                     "on one device, are wanted")
-        self.codes, self.scales, self.cols, self.padded = codes, scales, cols, p
-        self.lead = codes.shape[:-1]
+        self.cols, self.padded, self.lead = cols, p, form[:-1]
+        self.home, self._scales, self._split = codes, scales, codes.numel()
 
     def __reduce__(self):
-        return I8Tensor, (self.codes, self.scales, self.cols)
+        return _restored, (self.home, self._scales, tuple(self.lead), self.cols)
 
     def pointers(self) -> tuple[int, int]:
         """Where codes and scales are now (a caller may replace their memory, not their form)."""
-        codes, scales = self.codes, self.scales
-        if (codes.numel() != scales.numel() * self.padded or codes.shape[:-1] != self.lead
-                or not codes.is_contiguous() or not scales.is_contiguous()):
+        home, scales = self.home, self._scales
+        if scales is None:
+            start = home.data_ptr()
+            return start, start + self._split
+        if (home.numel() != self._split or scales.numel() * self.padded != self._split
+                or not home.is_contiguous() or not scales.is_contiguous()):
             _refuse("I8Tensor: its memory was replaced by some of another form")
-        return codes.data_ptr(), scales.data_ptr()
+        return home.data_ptr(), scales.data_ptr()
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._scales is not None:
+            return self.home
+        return self.home[:self._split].view(*self.lead, self.padded)
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is not None:
+            return self._scales
+        return self.home[self._split:].view(torch.float32).view(self.lead)
 
     @property
     def shape(self) -> torch.Size:
@@ -49,17 +68,33 @@ class I8Tensor:
 
     @property
     def device(self) -> torch.device:
-        return self.codes.device
+        return self.home.device
 
     def numel_bytes(self) -> int:
         return math.prod(self.lead) * (self.padded + 4)
 
 
 def _empty_i8(lead, cols, like) -> I8Tensor:
-    q = object.__new__(I8Tensor)  # of these there is nothing to check
-    q.cols, q.padded, q.lead = cols, (cols + 127) // 128 * 128, torch.Size(lead)
-    q.codes = like.new_empty((*lead, q.padded), dtype=torch.int8)
-    q.scales = like.new_empty(lead, dtype=torch.float32)
+    """`like`: any tensor on the device.  Of these forms there is nothing to check."""
+    q = object.__new__(I8Tensor)
+    q.cols, q.padded, q.lead, q._scales = cols, (cols + 127) // 128 * 128, lead, None
+    rows = math.prod(lead)
+    q._split = rows * q.padded  # a multiple of 128: the scales behind are aligned
+    q.home = like.new_empty(q._split + rows * 4, dtype=torch.int8)
+    return q
+
+
+def _restored(home, scales, lead, cols) -> I8Tensor:
+    """An I8Tensor of the parts that a copy or a file holds."""
+    if scales is not None:
+        return I8Tensor(home, scales, cols)
+    rows, padded = math.prod(lead), (cols + 127) // 128 * 128
+    if (home.dtype != torch.int8 or home.shape != (rows * (padded + 4),) or cols < 0
+            or not home.is_contiguous()):
+        _refuse("I8Tensor: int8 memory of codes and scales in one piece is wanted")
+    q = object.__new__(I8Tensor)
+    q.cols, q.padded, q.lead, q.home = cols, padded, torch.Size(lead), home
+    q._scales, q._split = None, rows * padded
     return q
 
 
@@ -79,13 +114,13 @@ def i8_quantize(x: torch.Tensor, stream=None) -> I8Tensor:
 
 def i8_dequantize(q: I8Tensor, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """The values that q holds, rounded once to dtype."""
-    if stream is not None or _b.elsewhere(q.codes):
+    if stream is not None or _b.elsewhere(q.home):
         return _b.on_stream(i8_dequantize, (q, dtype), stream)
     kind = TYPES.get(dtype)
-    if kind is None or not q.codes.is_cuda or q.cols == 0:
+    if kind is None or not q.home.is_cuda or q.cols == 0:
         _refuse("i8_dequantize: a nonempty row on the GPU and float32, float16 or bfloat16 are wanted")
-    y = q.codes.new_empty((*q.lead, q.cols), dtype=dtype)
-    _b.check(_b.lib().ec_i8_dequantize(*q.pointers(), q.scales.numel(), q.cols, y.data_ptr(), kind,
+    y = q.home.new_empty((*q.lead, q.cols), dtype=dtype)
+    _b.check(_b.lib().ec_i8_dequantize(*q.pointers(), y.numel() // q.cols, q.cols, y.data_ptr(), kind,
                                        q.cols, _b.current_stream(y)), "ec_i8_dequantize")
     return y
 
@@ -93,14 +128,14 @@ def i8_dequantize(q: I8Tensor, dtype: torch.dtype = torch.float32, stream=None) 
 def i8_product(a: I8Tensor, b: I8Tensor, dtype: torch.dtype = torch.bfloat16,
                stream=None) -> torch.Tensor:
     """a b^T [rows, cols] of a [rows, depth] and b [cols, depth], summed in whole numbers."""
-    if stream is not None or _b.elsewhere(a.codes):
+    if stream is not None or _b.elsewhere(a.home):
         return _b.on_stream(i8_product, (a, b, dtype), stream)
     kind = TYPES.get(dtype)
     if (kind is None or len(a.lead) != 1 or len(b.lead) != 1 or a.cols != b.cols or a.cols == 0
-            or b.lead[0] == 0 or not a.codes.is_cuda or a.codes.device != b.codes.device):
+            or b.lead[0] == 0 or not a.home.is_cuda or a.home.device != b.home.device):
         _refuse("i8_product: [rows, depth] and [cols, depth] on one GPU are wanted")
     rows, cols = a.lead[0], b.lead[0]
-    y = a.codes.new_empty((rows, cols), dtype=dtype)
+    y = a.home.new_empty((rows, cols), dtype=dtype)
     _b.check(_b.lib().ec_i8_product(*a.pointers(), rows, *b.pointers(), cols, a.padded,
                                     y.data_ptr(), kind, _b.current_stream(y)), "ec_i8_product")
     return y
@@ -110,16 +145,16 @@ def i8_experts_product(a: I8Tensor, b: I8Tensor, offsets: torch.Tensor,
                        dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """Rows a [rows, depth] sorted by expert, rows [offsets[e], offsets[e + 1]) times the weights of
     expert e, b [experts, cols, depth]; zeros in rows of no expert."""
-    if stream is not None or _b.elsewhere(a.codes):
+    if stream is not None or _b.elsewhere(a.home):
         return _b.on_stream(i8_experts_product, (a, b, offsets, dtype), stream)
     kind = TYPES.get(dtype)
     if (kind is None or len(a.lead) != 1 or len(b.lead) != 2 or a.cols != b.cols or a.cols == 0
-            or 0 in b.lead or not a.codes.is_cuda or a.codes.device != b.codes.device):
+            or 0 in b.lead or not a.home.is_cuda or a.home.device != b.home.device):
         _refuse("i8_experts_product: [rows, depth] and [experts, cols, depth] on one GPU are wanted")
     experts, cols = b.lead
-    _offsets(offsets, experts, a.codes.device, "i8_experts_product")
+    _offsets(offsets, experts, a.home.device, "i8_experts_product")
     rows = a.lead[0]
-    y = a.codes.new_empty((rows, cols), dtype=dtype)
+    y = a.home.new_empty((rows, cols), dtype=dtype)
     _b.check(_b.lib().ec_i8_product_experts(*a.pointers(), rows, *b.pointers(), cols, a.padded,
                                             offsets.data_ptr(), experts, y.data_ptr(), kind,
                                             _b.current_stream(y)), "ec_i8_product_experts")
@@ -129,7 +164,7 @@ def i8_experts_product(a: I8Tensor, b: I8Tensor, offsets: torch.Tensor,
 def _linear(x, w, offsets, experts, what):
     kind = _type(x, what)
     cols, depth = w.lead[-1], x.shape[-1]
-    if w.cols != depth or depth == 0 or 0 in w.lead or w.codes.device != x.device:
+    if w.cols != depth or depth == 0 or 0 in w.lead or w.home.device != x.device:
         _refuse(f"{what}: weights [.., cols, depth] on the device of x [.., depth] are wanted")
     r, stride = _rows(x)
     rows = r.shape[0]
@@ -137,7 +172,7 @@ def _linear(x, w, offsets, experts, what):
     y = x.new_empty((*x.shape[:-1], cols))
     need = L.ec_i8_linear_workspace_bytes(rows, depth, cols, experts)
     # held until the call is back: before, its kernels are not all enqueued
-    ws = w.codes.new_empty(need) if need else None
+    ws = w.home.new_empty(need, dtype=torch.int8) if need else None
     _b.check(L.ec_i8_linear(r.data_ptr(), kind, rows, depth, stride, *w.pointers(), cols,
                             offsets.data_ptr() if experts else None, experts, y.data_ptr(),
                             ws.data_ptr() if need else None, need,

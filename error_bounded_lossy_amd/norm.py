@@ -16,29 +16,31 @@ from .mx import TYPES, _refuse, _rows, _type
 
 
 def _inputs(x, weight, residual, what):
-    """x and the residual as rows with their strides, and the types."""
-    kind = _type(x, what)
-    wkind = _type(weight, what)
-    if (x.dim() == 0 or x.shape[-1] == 0 or weight.shape != x.shape[-1:]
-            or weight.device != x.device):
+    """x and the residual as rows with their strides, the contiguous weight, and the types."""
+    kind, wkind = _type(x, what), _type(weight, what)
+    cols = x.shape[-1] if x.dim() else 0
+    if cols == 0 or weight.shape != (cols,) or weight.device != x.device:
         _refuse(f"{what}: x [.., cols] and weight [cols] on one device are wanted")
-    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype
-                                 or residual.device != x.device):
-        _refuse(f"{what}: a residual of x's shape, type and device is wanted")
+    if not weight.is_contiguous():
+        weight = weight.contiguous()
     r, stride = _rows(x)
-    s, s_stride = (None, 0) if residual is None else _rows(residual)
-    return r, stride, s, s_stride, kind, weight.contiguous(), wkind
+    if residual is None:
+        return r, stride, None, 0, kind, weight, wkind
+    if (residual.shape != x.shape or residual.dtype != x.dtype
+            or residual.device != x.device):
+        _refuse(f"{what}: a residual of x's shape, type and device is wanted")
+    return r, stride, *_rows(residual), kind, weight, wkind
 
 
 def _norm(x, weight, eps, residual, saved, what):
     r, stride, s, s_stride, kind, weight, wkind = _inputs(x, weight, residual, what)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    h = None if s is None else torch.empty_like(y)
-    rstd = torch.empty(r.shape[0], dtype=torch.float32, device=x.device) if saved else None
+    rows, cols = r.shape
+    y, h = x.new_empty(x.shape), None if s is None else x.new_empty(x.shape)
+    rstd = x.new_empty(rows, dtype=torch.float32) if saved else None
     _b.check(_b.lib().ec_rms_norm(
-        r.data_ptr(), stride, None if s is None else s.data_ptr(), s_stride, kind, r.shape[0],
-        r.shape[1], weight.data_ptr(), wkind, eps, None if h is None else h.data_ptr(),
-        y.data_ptr(), rstd.data_ptr() if saved else None, _b.current_stream(x)), "ec_rms_norm")
+        r.data_ptr(), stride, None if s is None else s.data_ptr(), s_stride, kind, rows, cols,
+        weight.data_ptr(), wkind, eps, None if h is None else h.data_ptr(), y.data_ptr(),
+        rstd.data_ptr() if saved else None, _b.current_stream(x)), "ec_rms_norm")
     return y, h, rstd, weight
 
 
@@ -59,12 +61,14 @@ def rms_norm_i8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     if stream is not None or _b.elsewhere(x):
         return _b.on_stream(rms_norm_i8, (x, weight, eps, residual), stream)
     r, stride, s, s_stride, kind, weight, wkind = _inputs(x, weight, residual, "rms_norm_i8")
-    q: I8Tensor = _empty_i8(x.shape[:-1], x.shape[-1], x)
-    h = None if s is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    rows, cols = r.shape
+    q: I8Tensor = _empty_i8(x.shape[:-1], cols, x)
+    h = None if s is None else x.new_empty(x.shape)
+    at = q.home.data_ptr()
     _b.check(_b.lib().ec_rms_norm_i8(
-        r.data_ptr(), stride, None if s is None else s.data_ptr(), s_stride, kind, r.shape[0],
-        r.shape[1], weight.data_ptr(), wkind, eps, None if h is None else h.data_ptr(),
-        *q.pointers(), _b.current_stream(x)), "ec_rms_norm_i8")
+        r.data_ptr(), stride, None if s is None else s.data_ptr(), s_stride, kind, rows, cols,
+        weight.data_ptr(), wkind, eps, None if h is None else h.data_ptr(), at, at + q._split,
+        _b.current_stream(x)), "ec_rms_norm_i8")
     return q if h is None else (q, h)
 
 
@@ -94,21 +98,26 @@ def rms_norm_backward(dy: torch.Tensor, saved: RMSNormSaved, dh: torch.Tensor | 
     if stream is not None or _b.elsewhere(dy):
         return _b.on_stream(rms_norm_backward, (dy, saved, dh), stream)
     h, rstd, weight = saved.h, saved.rstd, saved.weight
-    _type(dy, "rms_norm_backward")
-    for t in (dy,) if dh is None else (dy, dh):
-        if t.shape != h.shape or t.dtype != h.dtype or t.device != h.device:
-            _refuse("rms_norm_backward: gradients of the forward's shape, type and device are wanted")
-    dy, h = dy.contiguous(), h.contiguous()
-    dh = None if dh is None else dh.contiguous()
-    dx, dweight = torch.empty_like(h), torch.empty_like(weight)
-    rows, cols = rstd.shape[0], h.shape[-1]
+    kind = _type(dy, "rms_norm_backward")
+    shape, device = h.shape, h.device
+    if (dy.shape != shape or dy.dtype != h.dtype or dy.device != device or dh is not None
+            and (dh.shape != shape or dh.dtype != h.dtype or dh.device != device)):
+        _refuse("rms_norm_backward: gradients of the forward's shape, type and device are wanted")
+    if not h.is_contiguous():
+        h = h.contiguous()
+    if not dy.is_contiguous():
+        dy = dy.contiguous()
+    if dh is not None and not dh.is_contiguous():
+        dh = dh.contiguous()
+    dx, dweight = h.new_empty(shape), weight.new_empty(weight.shape)
+    rows, cols = rstd.shape[0], shape[-1]
     L = _b.lib()
     need = L.ec_rms_norm_backward_workspace_bytes(rows, cols)
     # held until the call is back: before, its kernels are not all enqueued
     ws = h.new_empty(need, dtype=torch.uint8) if need else None
     _b.check(L.ec_rms_norm_backward(
-        dy.data_ptr(), h.data_ptr(), None if dh is None else dh.data_ptr(), TYPES[h.dtype], rows,
-        cols, rstd.data_ptr(), weight.data_ptr(), TYPES[weight.dtype], dx.data_ptr(),
+        dy.data_ptr(), h.data_ptr(), None if dh is None else dh.data_ptr(), kind, rows, cols,
+        rstd.data_ptr(), weight.data_ptr(), TYPES[weight.dtype], dx.data_ptr(),
         dweight.data_ptr(), ws.data_ptr() if need else None, need, _b.current_stream(dy)),
         "ec_rms_norm_backward")
     return dx, dweight
