@@ -72,14 +72,32 @@ def rms_norm_i8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     return q if h is None else (q, h)
 
 
+def _version(t):
+    """How often torch counts that t was written to (None: it does not count, for an inference
+    tensor and in a graph, whose replays the count knows nothing of)."""
+    return None if t.is_inference() or _b.capturing(t) else t._version
+
+
 class RMSNormSaved:
     """What the backward pass of the norm needs: h (the sum, or x itself), 1 / sqrt(mean(h^2) +
-    eps) of each row, and the weight.  None of them may be written to until then."""
+    eps) of each row, and the weight.  They have to keep their values until then: writes that torch
+    counts are found."""
 
-    __slots__ = ("h", "rstd", "weight")
+    __slots__ = ("h", "rstd", "weight", "versions")
 
     def __init__(self, h, rstd, weight):
         self.h, self.rstd, self.weight = h, rstd, weight
+        self.versions = _version(h), _version(weight)
+
+    def same_values(self) -> bool:
+        h, weight = self.versions
+        return ((h is None or h == self.h._version)
+                and (weight is None or weight == self.weight._version))
+
+    def __reduce__(self):
+        if not self.same_values():
+            _refuse("RMSNormSaved: its tensors were written to since the forward pass")
+        return RMSNormSaved, (self.h, self.rstd, self.weight)
 
 
 def rms_norm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -103,6 +121,8 @@ def rms_norm_backward(dy: torch.Tensor, saved: RMSNormSaved, dh: torch.Tensor | 
     if (dy.shape != shape or dy.dtype != h.dtype or dy.device != device or dh is not None
             and (dh.shape != shape or dh.dtype != h.dtype or dh.device != device)):
         _refuse("rms_norm_backward: gradients of the forward's shape, type and device are wanted")
+    if not saved.same_values():
+        _refuse("rms_norm_backward: what was saved was written to since the forward pass")
     if not h.is_contiguous():
         h = h.contiguous()
     if not dy.is_contiguous():
