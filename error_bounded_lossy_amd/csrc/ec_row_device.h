@@ -118,7 +118,8 @@ __device__ __forceinline__ uint32_t magnitude_of_floats(const float (&f)[8]) {
 
 // Lanes for a row of `chunks` pieces: a power of two while that makes up to 256
 // threads of `each` pieces, then a workgroup of as many threads (a multiple of `unit`)
-// as give a lane `most` pieces, then up to 512 threads of up to 4, then rounds.
+// as give a lane `most` pieces, then up to 512 threads of up to 4 (with most = 1: 512),
+// then rounds.
 inline RowShape row_shape(uint64_t rows, uint64_t cols, uint64_t chunks, uint32_t each,
                           uint32_t most, uint32_t unit, uint32_t& pieces, uint32_t& threads) {
   RowShape s{};
@@ -129,7 +130,7 @@ inline RowShape row_shape(uint64_t rows, uint64_t cols, uint64_t chunks, uint32_
   threads = kRowThreads;
   if (each * lanes < chunks) {
     lanes = ceil_div(ceil_div(chunks, most), unit) * unit;
-    if (lanes > kMostThreads) lanes = ceil_div(ceil_div(chunks, 4), unit) * unit;
+    if (lanes > kMostThreads && most > 1) lanes = ceil_div(ceil_div(chunks, 4), unit) * unit;
     if (lanes > kMostThreads) lanes = kMostThreads;
     s.shift = kWhole;
     threads = (uint32_t)lanes;

@@ -32,10 +32,15 @@ def _inputs(x, weight, residual, what):
     return r, stride, *_rows(residual), kind, weight, wkind
 
 
+def _like(x):
+    """A contiguous tensor of x's form (torch's own empty_like takes less time, but keeps strides)."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
 def _norm(x, weight, eps, residual, saved, what):
     r, stride, s, s_stride, kind, weight, wkind = _inputs(x, weight, residual, what)
     rows, cols = r.shape
-    y, h = x.new_empty(x.shape), None if s is None else x.new_empty(x.shape)
+    y, h = _like(x), None if s is None else _like(x)
     rstd = x.new_empty(rows, dtype=torch.float32) if saved else None
     _b.check(_b.lib().ec_rms_norm(
         r.data_ptr(), stride, None if s is None else s.data_ptr(), s_stride, kind, rows, cols,
@@ -63,19 +68,13 @@ def rms_norm_i8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     r, stride, s, s_stride, kind, weight, wkind = _inputs(x, weight, residual, "rms_norm_i8")
     rows, cols = r.shape
     q: I8Tensor = _empty_i8(x.shape[:-1], cols, x)
-    h = None if s is None else x.new_empty(x.shape)
+    h = None if s is None else _like(x)
     at = q.home.data_ptr()
     _b.check(_b.lib().ec_rms_norm_i8(
         r.data_ptr(), stride, None if s is None else s.data_ptr(), s_stride, kind, rows, cols,
         weight.data_ptr(), wkind, eps, None if h is None else h.data_ptr(), at, at + q._split,
         _b.current_stream(x)), "ec_rms_norm_i8")
     return q if h is None else (q, h)
-
-
-def _version(t):
-    """How often torch counts that t was written to (None: it does not count, for an inference
-    tensor and in a graph, whose replays the count knows nothing of)."""
-    return None if t.is_inference() or _b.capturing(t) else t._version
 
 
 class RMSNormSaved:
@@ -87,7 +86,11 @@ class RMSNormSaved:
 
     def __init__(self, h, rstd, weight):
         self.h, self.rstd, self.weight = h, rstd, weight
-        self.versions = _version(h), _version(weight)
+        # How often torch counts that they were written to (None: it does not count, for an
+        # inference tensor and in a graph, whose replays the count knows nothing of).
+        self.versions = None, None
+        if not _b.capturing(h):
+            self.versions = tuple(None if t.is_inference() else t._version for t in (h, weight))
 
     def same_values(self) -> bool:
         h, weight = self.versions
@@ -129,7 +132,7 @@ def rms_norm_backward(dy: torch.Tensor, saved: RMSNormSaved, dh: torch.Tensor | 
         dy = dy.contiguous()
     if dh is not None and not dh.is_contiguous():
         dh = dh.contiguous()
-    dx, dweight = h.new_empty(shape), weight.new_empty(weight.shape)
+    dx, dweight = torch.empty_like(h), torch.empty_like(weight)
     rows, cols = rstd.shape[0], shape[-1]
     L = _b.lib()
     need = L.ec_rms_norm_backward_workspace_bytes(rows, cols)
