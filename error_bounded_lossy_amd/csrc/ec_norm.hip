@@ -30,7 +30,10 @@ struct Norm {
 
 // One pass over x and the residual: the row stays in registers (up to 16384
 // elements; longer rows are read again from h, or x, in each pass).  The weights
-// are asked for before the sum is known.
+// are asked for before the sum is known (one row of 8192 into 8 bits: 4.1 us, 6.3
+// with them behind the sum and 256 lanes).  Bound by memory: 16384 x 4096 bf16 with
+// residual 86 us (6.2 TB/s of bytes read and written; a copy of 1 GiB 5.1), 8200 x
+// 5120 into 8 bits 61 us (4.8 TB/s).
 template <typename T, int PIECES, bool EIGHT_BITS>
 __global__ __launch_bounds__(kMostThreads) void rms_norm(const Norm p, RowShape s) {
   __shared__ float sums[kMostWaves];
@@ -153,8 +156,11 @@ struct Back {
   float* parts;  // dweight's parts [gridDim * slots][cols]; NULL: another kernel sums it
 };
 
-// A workgroup takes every gridDim-th set of rows and adds up what they give to
-// dweight in registers; the next set's rows are on their way while it works on one.
+// dx = rstd (w dy - n mean(w dy n)) + dh with n = h rstd: the mean is one sum over the
+// row.  A workgroup takes every gridDim-th set of rows and adds up what they give to
+// dweight in registers; the next set's rows are on their way while it works on one
+// (without: 16384 x 4096 bf16 141 us, with the column sums, for 114).  Bound by memory:
+// 117 us of it in this kernel among others, 4.6 TB/s.
 template <typename T, int PIECES>
 __global__ __launch_bounds__(kMostThreads) void rms_norm_back(const Back p, RowShape s) {
   __shared__ float sums[2][kMostWaves];
@@ -262,7 +268,8 @@ __global__ __launch_bounds__(kMostThreads) void rms_norm_back(const Back p, RowS
 constexpr uint32_t kSumCols = 32, kSumSlices = 32, kSumAhead = 8;
 
 // Column sums of [parts][cols]: 32 columns a workgroup, their rows in 32 slices
-// that are joined in order.
+// that are joined in order, 8 rows of a slice on their way at a time (512 x 4096: 4.9
+// us; one at a time, of 1024 parts, 13).
 struct PartRows {
   const float* parts;
   uint64_t rows;
