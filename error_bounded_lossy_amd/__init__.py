@@ -141,6 +141,8 @@ def lib():
         ("ec_i8_quantize", st, (vp, i, u64, u64, u64, vp, vp, vp)),
         ("ec_i8_dequantize", st, (vp, vp, u64, u64, vp, i, u64, vp)),
         ("ec_i8_product", st, (vp, vp, u64, vp, vp, u64, u64, vp, i, vp)),
+        ("ec_i8_product_parts_bytes", sz, (u64, u64, u64)),
+        ("ec_i8_product_parts", st, (vp, vp, u64, vp, vp, u64, u64, vp, i, vp, sz, vp)),
         ("ec_i8_product_experts", st, (vp, vp, u64, vp, vp, u64, u64, vp, u32, vp, i, vp)),
         ("ec_i8_product_tile", u32, (u64, u64, u64, i, u32)),
         ("ec_i8_linear_workspace_bytes", sz, (u64, u64, u64, u32)),

@@ -27,6 +27,7 @@ struct Product {
   uint32_t depth;  // codes of a stored row
   uint32_t experts;
   uint32_t m_tiles, n_tiles;
+  uint32_t parts;  // of the contraction, of T = int32_t
 };
 
 // ---------------------------------------------------------------- tiles
@@ -115,10 +116,16 @@ __device__ __forceinline__ void multiply(const i32x4 (&a)[M], const i32x4 (&b)[N
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// With T = int32_t, a workgroup takes one of p.parts parts of the contraction, and y
+// [parts][rows][part_pitch(cols)] holds the parts' sums, which i8_join adds: the same
+// whole numbers in any order.
+//
 // STAGES: 2 of the largest tile (of one line each they fill LDS) and where two
 // workgroups share a unit; 4 where there is a unit for each (512 x 8192 x 8192 as tiles
 // of 128 41 us, with 2 stages 45; 2048 x 4096 x 4096 45 and 36), or the tile is small (8
 // stages of tiles of 64, 77 x 2500 x 1111: 5.9 us, 4: 5.2).
+__host__ __device__ uint32_t part_pitch(uint32_t cols) { return (cols + 63) / 64 * 64; }
+
 template <int FM, int FN, int STAGES, typename T, int MODE, bool PAST>
 __global__ __launch_bounds__(256, STAGES * FM * FN >= 16 ? 1 : 2) void i8_tiles(const Product p) {
   constexpr int BM = 64 * FM, BN = 64 * FN, kWaves = 4;
@@ -135,8 +142,9 @@ __global__ __launch_bounds__(256, STAGES * FM * FN >= 16 ? 1 : 2) void i8_tiles(
   // the tiles that groups have, not the most they could have: each XCD gets its share
   uint32_t m_tiles = p.m_tiles;
   if (MODE == kExperts) m_tiles = min(m_tiles, used_tiles(p.offsets, p.experts, p.rows, kShift));
+  constexpr bool kParts = std::is_same_v<T, int32_t>;
   uint32_t t, set = 0;
-  if (!dealt(m_tiles * p.n_tiles, 1, t, set)) return;
+  if (!dealt(m_tiles * p.n_tiles, kParts ? p.parts : 1, t, set)) return;
   // in an XCD's run, 8 tiles along the rows share a column tile
   const uint32_t width = 8 * p.n_tiles, band = t / width;
   const uint32_t high = min(m_tiles - band * 8, 8u);
@@ -185,13 +193,21 @@ __global__ __launch_bounds__(256, STAGES * FM * FN >= 16 ? 1 : 2) void i8_tiles(
   for (int i = 0; i < LB; i++)
     ob[i] = min((wave * LB + i) * 8 + (lane >> 3), n_last) * pitch + chunk * 16;
   constexpr int kLoads = LA + LB;
-  const uint32_t stages = __builtin_amdgcn_readfirstlane(p.depth / 128);
+  uint32_t stages = __builtin_amdgcn_readfirstlane(p.depth / 128), begin = 0;
+  uint32_t y_pitch = p.cols, y_cols = p.cols;
+  if constexpr (kParts) {
+    const uint32_t each = (stages + p.parts - 1) / p.parts;  // the last one may have fewer
+    begin = __builtin_amdgcn_readfirstlane(set * each);
+    stages = min(each, stages - begin);
+    y_pitch = y_cols = part_pitch(p.cols);
+    y += set * p.rows * y_pitch;
+  }
   // Past the last stage it is loaded again, so that every turn below does the
   // same and waits for the same number of loads.  Part i of 2 FM: two loads behind every row
   // of multiplications (8192^3: 494 us; four behind the first half of them 509, eight
   // behind the first quarter 530).
-  const __amdgpu_buffer_rsrc_t ra = buffer_at(p.a.codes + m0 * pitch);
-  const __amdgpu_buffer_rsrc_t rb = buffer_at(bc + (uint64_t)n0 * pitch);
+  const __amdgpu_buffer_rsrc_t ra = buffer_at(p.a.codes + m0 * pitch + begin * 128);
+  const __amdgpu_buffer_rsrc_t rb = buffer_at(bc + (uint64_t)n0 * pitch + begin * 128);
   auto load = [&](St& st, uint32_t stage, int part) __attribute__((always_inline)) {
     const uint32_t c = __builtin_amdgcn_readfirstlane(min(stage, stages - 1)) * 128;
 #pragma unroll
@@ -211,8 +227,9 @@ __global__ __launch_bounds__(256, STAGES * FM * FN >= 16 ? 1 : 2) void i8_tiles(
   at.a = (wm * 32 * FM + r) * 128 + (g ^ (r & 7)) * 16;
   at.b = (wn * 32 * FN + r) * 128 + (g ^ (r & 7)) * 16;
 
-  for (uint32_t i = threadIdx.x; i < BM + BN; i += 256)
-    scales[i] = i < BM ? p.a.scales[m0 + min(i, m_last)] : bs[n0 + min(i - BM, n_last)];
+  if constexpr (!kParts)
+    for (uint32_t i = threadIdx.x; i < BM + BN; i += 256)
+      scales[i] = i < BM ? p.a.scales[m0 + min(i, m_last)] : bs[n0 + min(i - BM, n_last)];
 
   i32x4 acc[2 * FM][2 * FN];
 #pragma unroll
@@ -292,8 +309,10 @@ __global__ __launch_bounds__(256, STAGES * FM * FN >= 16 ? 1 : 2) void i8_tiles(
         __builtin_memcpy(sb, __builtin_assume_aligned(scales + BM + wn * 32 * FN + col, 16), 16);
         T v[4];
 #pragma unroll
-        for (int u = 0; u < 4; u++)
-          v[u] = (T)in_fp32<T>((float)acc[2 * i + h][j][u] * sa * sb[u]);
+        for (int u = 0; u < 4; u++) {
+          if constexpr (kParts) v[u] = acc[2 * i + h][j][u];
+          else v[u] = (T)in_fp32<T>((float)acc[2 * i + h][j][u] * sa * sb[u]);
+        }
         __builtin_memcpy(out + (h * 16 + r) * kPitch + col * sizeof(T), v, sizeof(v));
       }
     }
@@ -307,19 +326,39 @@ __global__ __launch_bounds__(256, STAGES * FM * FN >= 16 ? 1 : 2) void i8_tiles(
       T v[kE];
       __builtin_memcpy(v, __builtin_assume_aligned(out + row * kPitch + col * sizeof(T), 16), 16);
       if (m < m_end) {
-        T* to = y + m * p.cols + nw + col;
-        if (nw + col + kE <= p.cols) {
+        T* to = y + m * y_pitch + nw + col;
+        if (nw + col + kE <= y_cols) {
           store16<PAST>(to, v);
         } else {
 #pragma unroll
           for (uint32_t u = 0; u < kE; u++)
-            if (nw + col + u < p.cols) to[u] = v[u];
+            if (nw + col + u < y_cols) to[u] = v[u];
         }
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
+}
+
+// What the parts of a contraction sum to, scaled and rounded as a tile's results are;
+// a thread takes four columns of a row.
+template <typename T>
+__global__ __launch_bounds__(256) void i8_join(const Product p, T* y) {
+  const uint32_t pitch = part_pitch(p.cols), quads = pitch / 4;
+  const uint64_t i = (uint64_t)block_number() * 256 + threadIdx.x;
+  if (i >= p.rows * quads) return;
+  const uint64_t row = i / quads;
+  const uint32_t col = (uint32_t)(i - row * quads) * 4;
+  const i32x4* from = (const i32x4*)p.y + i;
+  i32x4 sum = {};
+#pragma unroll 4
+  for (uint32_t s = 0; s < p.parts; s++) sum += from[s * p.rows * quads];
+  const float sa = p.a.scales[row];
+#pragma unroll
+  for (int u = 0; u < 4; u++)
+    if (col + u < p.cols)
+      y[row * p.cols + col + u] = (T)in_fp32<T>((float)sum[u] * sa * p.b.scales[col + u]);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -524,6 +563,55 @@ uint64_t rows_first(uint64_t rows, uint64_t cols, uint64_t depth, size_t bytes) 
   return t.cost[0] + 6 * 1024 + cost(rows - main) < cost(rows) ? main : 0;
 }
 
+// Parts of the contraction, 1: the tiles take it whole.  A workgroup of a small tile
+// gets a stage of 128 codes in 0.22 to 0.27 us however few of them there are, so with
+// few tiles the units that are left take parts of it: as many as fill all once, of one
+// row tile, whose parts are small, twice, with 8 stages at least.  The sums' way through
+// memory and the second kernel cost 4 us, and 5 of the host, so 32 stages have to be
+// saved.  Rows x contraction x columns, us in a graph, whole and in parts, weights out of
+// memory:
+//   32 x 16384 x 4096: 36.4, 19.5; 64: 40.0, 22.2; 128: 39.9, 29.6
+//   32 x 8192 x 8192: 22.8, 19.6; 32 x 8192 x 1024: 13.1, 8.1; 256: 13.6, 10.7
+//   32 x 5120 x 2048: 12.6, 8.5; 4096 x 4096 (24 saved): 12.0, 10.1, but 11.7, 15.2 eager
+//   128 x 4096 x 4096 (16 saved): 12.9, 13.7; twice full, 128 x 8192 x 8192: 24.5, 30.3;
+//   4 stages at least, 32 x 4096 x 4096: 12.3
+uint32_t parts_of(uint64_t rows, uint64_t cols, uint64_t depth) {
+  if (rows <= kFewRows || rows > EC_I8_MOST_PARTS_ROWS || cols == 0 || cols > EC_MX_MAX_ROWS)
+    return 1;
+  const uint64_t tiles = ceil_div(rows, 64) * ceil_div(cols, 64), stages = depth / 128;
+  uint64_t most = (rows <= 64 ? 512 : 256) / tiles;
+  if (most > stages / 8) most = stages / 8;
+  if (most < 2) return 1;
+  const uint64_t each = ceil_div(stages, most);
+  if (stages - each < 32) return 1;
+  return (uint32_t)ceil_div(stages, each);  // none is empty
+}
+uint64_t part_bytes(uint64_t rows, uint64_t cols, uint64_t depth) {
+  const uint32_t parts = parts_of(rows, cols, depth);
+  return parts > 1 ? parts * rows * part_pitch((uint32_t)cols) * 4 : 0;
+}
+
+template <typename T>
+ec_status join_as(const Product& p, void* y, hipStream_t s) {
+  const uint64_t blocks = ceil_div(p.rows * (part_pitch(p.cols) / 4), 256);
+  hipLaunchKernelGGL((i8_join<T>), grid_of(blocks), dim3(256), 0, s, p, (T*)y);
+  return launched();
+}
+ec_status product_in_parts(Product p, int type, void* workspace, hipStream_t s) {
+  void* y = p.y;
+  p.y = workspace, p.parts = parts_of(p.rows, p.cols, p.depth);
+  p.n_tiles = (uint32_t)ceil_div(p.cols, 64), p.m_tiles = (uint32_t)ceil_div(p.rows, 64);
+  const uint64_t blocks = ceil_div((uint64_t)p.m_tiles * p.n_tiles, 8) * 8 * p.parts;
+  hipLaunchKernelGGL((i8_tiles<1, 1, 4, int32_t, kDense, false>), grid_of(blocks), dim3(256), 0, s, p);
+  const ec_status st = launched();
+  if (st != EC_OK) return st;
+  switch (type) {
+    case EC_TYPE_F32: return join_as<float>(p, y, s);
+    case EC_TYPE_F16: return join_as<f16_t>(p, y, s);
+    default: return join_as<bf16_t>(p, y, s);
+  }
+}
+
 template <typename T, int MODE>
 ec_status tiles_of(const Product& p, hipStream_t s) {
   const Tiles t = tiles_for(MODE, p.rows, p.cols, p.depth, p.experts, sizeof(T));
@@ -567,14 +655,16 @@ ec_status product_as(const Product& p, hipStream_t s) {
   return p.experts ? tiles_of<T, kExperts>(p, s) : tiles_of<T, kDense>(p, s);
 }
 
-ec_status product(Product p, int type, hipStream_t s) {
+ec_status product(Product p, int type, void* workspace, hipStream_t s) {
+  if (workspace && !p.experts && parts_of(p.rows, p.cols, p.depth) > 1)
+    return product_in_parts(p, type, workspace, s);
   const size_t bytes = type_bytes(type);
   if (const uint64_t first = p.experts ? 0 : rows_first(p.rows, p.cols, p.depth, bytes)) {
     Product rest = p;
     rest.a = {p.a.codes + first * p.depth, p.a.scales + first};
     rest.y = (uint8_t*)p.y + first * p.cols * bytes;
     rest.rows = p.rows - first;
-    const ec_status st = product(rest, type, s);
+    const ec_status st = product(rest, type, nullptr, s);
     if (st != EC_OK) return st;
     p.rows = first;
   }
@@ -612,8 +702,12 @@ Product product_of(const void* a_codes, const void* a_scales, uint64_t rows, con
   return p;
 }
 
-// Codes of the workspace of a linear layer; the scales are behind them.
+// Codes of the workspace of a linear layer; the scales are behind them, then the sums of
+// the contraction's parts.
 uint64_t code_bytes(uint64_t rows, uint64_t depth) { return rows * ec_mx_padded(depth); }
+uint64_t parts_begin(uint64_t rows, uint64_t depth) {
+  return code_bytes(rows, depth) + ceil_div(rows * 4, 16) * 16;
+}
 
 }  // namespace
 
@@ -625,7 +719,25 @@ ec_status ec_i8_product(const void* a_codes, const void* a_scales, uint64_t rows
   const ec_status st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, y, type);
   if (st != EC_OK || rows == 0) return st;
   return product(product_of(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, nullptr, 0, y),
-                 type, (hipStream_t)stream);
+                 type, nullptr, (hipStream_t)stream);
+}
+
+size_t ec_i8_product_parts_bytes(uint64_t rows, uint64_t cols, uint64_t depth) {
+  if (depth % 128 != 0 || depth > EC_I8_MAX_DEPTH) return 0;  // no such product
+  return part_bytes(rows, cols, depth);
+}
+
+ec_status ec_i8_product_parts(const void* a_codes, const void* a_scales, uint64_t rows,
+                              const void* b_codes, const void* b_scales, uint64_t cols,
+                              uint64_t depth, void* y, int type, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  const ec_status st = check(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, y, type);
+  if (st != EC_OK || rows == 0) return st;
+  const size_t need = part_bytes(rows, cols, depth);
+  if (!aligned(workspace, 16) || (need && !workspace)) return EC_ERR_INVALID;
+  if (workspace_bytes < need) return EC_ERR_CAPACITY;
+  return product(product_of(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, nullptr, 0, y),
+                 type, workspace, (hipStream_t)stream);
 }
 
 ec_status ec_i8_product_experts(const void* a_codes, const void* a_scales, uint64_t rows,
@@ -637,7 +749,7 @@ ec_status ec_i8_product_experts(const void* a_codes, const void* a_scales, uint6
   if (st != EC_OK || rows == 0) return st;
   return product(product_of(a_codes, a_scales, rows, b_codes, b_scales, cols, depth, offsets,
                             experts, y),
-                 type, (hipStream_t)stream);
+                 type, nullptr, (hipStream_t)stream);
 }
 
 uint32_t ec_i8_product_tile(uint64_t rows, uint64_t cols, uint64_t depth, int type,
@@ -650,9 +762,10 @@ uint32_t ec_i8_product_tile(uint64_t rows, uint64_t cols, uint64_t depth, int ty
 
 size_t ec_i8_linear_workspace_bytes(uint64_t rows, uint64_t depth, uint64_t cols,
                                     uint32_t experts) {
-  (void)cols;
-  if (few_quantizing(rows, ec_mx_padded(depth), experts)) return 0;
-  return code_bytes(rows, depth) + rows * 4;
+  const uint64_t padded = ec_mx_padded(depth);
+  if (few_quantizing(rows, padded, experts)) return 0;
+  const uint64_t parts = experts ? 0 : part_bytes(rows, cols, padded);
+  return parts ? parts_begin(rows, depth) + parts : code_bytes(rows, depth) + rows * 4;
 }
 
 ec_status ec_i8_linear(const void* x, int type, uint64_t rows, uint64_t depth, uint64_t stride,
@@ -688,7 +801,7 @@ ec_status ec_i8_linear(const void* x, int type, uint64_t rows, uint64_t depth, u
   if (st != EC_OK) return st;
   return product(product_of(codes, scales, rows, w_codes, w_scales, cols, padded, offsets, experts,
                             y),
-                 type, (hipStream_t)stream);
+                 type, codes + parts_begin(rows, depth), (hipStream_t)stream);
 }
 
 }  // extern "C"

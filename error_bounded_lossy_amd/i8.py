@@ -14,6 +14,9 @@ import torch
 from . import _binding as _b
 from .mx import TYPES, _offsets, _refuse, _rows, _type
 
+# of a product that may be taken in parts of its contraction (include/ec_i8.h)
+MOST_PARTS_ROWS = 256
+
 
 class I8Tensor:
     """A tensor in the 8-bit form along its last dimension, of `cols` elements: codes, int8
@@ -136,6 +139,14 @@ def i8_product(a: I8Tensor, b: I8Tensor, dtype: torch.dtype = torch.bfloat16,
         _refuse("i8_product: [rows, depth] and [cols, depth] on one GPU are wanted")
     rows, cols = a.lead[0], b.lead[0]
     y = a.home.new_empty((rows, cols), dtype=dtype)
+    need = _b.lib().ec_i8_product_parts_bytes(rows, cols, a.padded) if 16 < rows <= MOST_PARTS_ROWS else 0
+    if need:
+        # held until the call is back: before, its kernels are not all enqueued
+        ws = a.home.new_empty(need, dtype=torch.int8)
+        _b.check(_b.lib().ec_i8_product_parts(*a.pointers(), rows, *b.pointers(), cols, a.padded,
+                                              y.data_ptr(), kind, ws.data_ptr(), need,
+                                              _b.current_stream(y)), "ec_i8_product_parts")
+        return y
     _b.check(_b.lib().ec_i8_product(*a.pointers(), rows, *b.pointers(), cols, a.padded,
                                     y.data_ptr(), kind, _b.current_stream(y)), "ec_i8_product")
     return y

@@ -51,6 +51,18 @@ ec_status ec_i8_product(const void* a_codes, const void* a_scales, uint64_t rows
                         const void* b_codes, const void* b_scales, uint64_t cols, uint64_t depth,
                         void* y, int type, void* stream);
 
+/* The same in parts of the contraction, where few rows and a long one leave most
+ * of the GPU idle: the workspace (16-byte aligned, may be NULL where the size is
+ * 0) holds ec_i8_product_parts_bytes(...) bytes, which is 0 where the product is
+ * taken in one part, as of more than EC_I8_MOST_PARTS_ROWS rows.  The results are
+ * the same. */
+#define EC_I8_MOST_PARTS_ROWS 256u
+size_t ec_i8_product_parts_bytes(uint64_t rows, uint64_t cols, uint64_t depth);
+ec_status ec_i8_product_parts(const void* a_codes, const void* a_scales, uint64_t rows,
+                              const void* b_codes, const void* b_scales, uint64_t cols,
+                              uint64_t depth, void* y, int type, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* y [rows][cols]: row r of group e is a[r] b[e]^T with b [experts][cols][depth];
  * rows of no group are zeros. */
 ec_status ec_i8_product_experts(const void* a_codes, const void* a_scales, uint64_t rows,

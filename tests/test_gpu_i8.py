@@ -130,6 +130,31 @@ def test_rows_past_whole_tiles(rows, dtype):  # some in a launch of their own
     assert torch.equal(ec.i8_product(a, b, dtype), R.i8_product(a.codes, a.scales, b.codes, b.scales, dtype))
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,depth,cols", [(17, 5120, 1), (33, 20000, 40), (64, 6000, 130), (64, 8192, 8100), (65, 8100, 1000),
+                                             (200, 9000, 501), (256, 16384, 250), (256, 5249, 66)])
+def test_product_in_parts_of_the_contraction(rows, depth, cols, dtype):
+    a, b = codes(rows, rows, depth), codes(cols + 7, cols, depth)
+    assert ec.lib().ec_i8_product_parts_bytes(rows, cols, a.padded) > 0
+    want = R.i8_product(a.codes, a.scales, b.codes, b.scales, dtype)
+    assert torch.equal(ec.i8_product(a, b, dtype), want)
+    x = values(1, rows, depth + 3, dtype=dtype)[:, :depth]
+    q = ec.i8_quantize(x)
+    assert torch.equal(ec.i8_linear(x, b), R.i8_product(q.codes, q.scales, b.codes, b.scales, dtype))
+
+
+def test_what_is_not_finite_in_parts_of_the_contraction():
+    x, w = values(1, 40, 9000, dtype=torch.float32), ec.i8_quantize(values(2, 50, 9000))
+    assert ec.lib().ec_i8_product_parts_bytes(40, 50, 9088) > 0
+    x[3, 8999], x[7, 0], x[11] = math.nan, -math.inf, 0
+    y = ec.i8_linear(x, w)
+    bad = torch.zeros(40, dtype=torch.bool, device="cuda")
+    bad[[3, 7]] = True
+    assert torch.equal(y.isnan(), bad[:, None].expand(40, 50)) and not y[11].any()
+    q = ec.i8_quantize(x)
+    assert same(y, R.i8_product(q.codes, q.scales, w.codes, w.scales, torch.float32))
+
+
 def split(rows, experts, seed, left=0):
     g = torch.Generator().manual_seed(seed)
     cuts = torch.randint(0, rows - left + 1, (experts - 1,), generator=g).sort().values

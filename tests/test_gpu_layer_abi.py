@@ -48,6 +48,25 @@ def test_products_write_nothing_outside(rows, depth, cols, dtype):
     assert torch.equal(y, R.i8_product(a.codes, a.scales, w.codes, w.scales, dtype))
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,depth,cols", [(17, 64, 65), (17, 5100, 65), (47, 20000, 3), (130, 8200, 131), (256, 5300, 257)])
+def test_products_in_parts_write_nothing_outside(rows, depth, cols, dtype):
+    a, w, kind = i8(rows, depth), i8(cols, depth, 2), KINDS[dtype]
+    b = Buffers()
+    y, z = b(dtype, rows, cols), b(dtype, rows, cols)
+    need = ec.lib().ec_i8_product_parts_bytes(rows, cols, a.padded)
+    assert (need > 0) == (depth > 64)
+    call("ec_i8_product_parts", a.codes, a.scales, rows, w.codes, w.scales, cols, a.padded, y, kind, b(torch.uint8, need) if need else None, need)
+    x = values(1, rows, depth).to(dtype)
+    more = ec.lib().ec_i8_linear_workspace_bytes(rows, depth, cols, 0)
+    assert more >= need + rows * (a.padded + 4)
+    call("ec_i8_linear", x, kind, rows, depth, depth, w.codes, w.scales, cols, None, 0, z, b(torch.uint8, more), more)
+    b.done()
+    q = ec.i8_quantize(x)
+    assert torch.equal(y, R.i8_product(a.codes, a.scales, w.codes, w.scales, dtype))
+    assert torch.equal(z, R.i8_product(q.codes, q.scales, w.codes, w.scales, dtype))
+
+
 @pytest.mark.parametrize("tokens,k,cols", [(50, 2, 96), (33, 4, 33), (300, 3, 1111), (7, 1, 9000)])
 def test_places_and_offsets_out_of_range_write_nothing_outside(tokens, k, cols):
     rows, experts = tokens * k, 4

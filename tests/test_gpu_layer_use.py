@@ -185,6 +185,34 @@ def test_two_graphs_with_workspaces():
         assert torch.equal(y, ec.i8_linear(a, w)) and torch.equal(z, ec.i8_linear(b, w))
 
 
+def test_two_graphs_and_two_streams_with_parts_of_a_contraction():
+    a, b, w = randn(1, 100, 9000), randn(2, 60, 9000), ec.i8_quantize(randn(3, 200, 9000))
+    q = ec.i8_quantize(a)
+    assert ec.lib().ec_i8_product_parts_bytes(100, 200, q.padded) and ec.lib().ec_i8_product_parts_bytes(60, 200, q.padded)
+    ec.i8_linear(a, w)
+    torch.cuda.synchronize()
+    one, two = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(one):
+        y, p = ec.i8_linear(a, w), ec.i8_product(q, w)
+    with torch.cuda.graph(two):
+        z = ec.i8_linear(b, w)
+    side = torch.cuda.Stream()
+    for seed in range(4):
+        a.copy_(randn(seed + 10, 100, 9000))
+        b.copy_(randn(seed + 20, 60, 9000))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            two.replay()
+        one.replay()
+        eager = ec.i8_linear(b, w)
+        other = ec.i8_linear(a, w, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(y, ec.i8_linear(a, w)) and torch.equal(z, ec.i8_linear(b, w))
+        assert torch.equal(eager, z) and torch.equal(other, y) and torch.equal(p, ec.i8_product(q, w))
+        s = ec.i8_quantize(b)
+        assert torch.equal(z, R.i8_product(s.codes, s.scales, w.codes, w.scales, b.dtype))
+
+
 # ---------------------------------------------------------------- streams, threads, copies
 
 

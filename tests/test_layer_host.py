@@ -48,6 +48,34 @@ def test_products(L):
     assert e(F, F, 1, F, F, 8, 64, F, 2, F, BF16, None) == INVALID
 
 
+def test_products_in_parts(L):
+    p, size = L.ec_i8_product_parts, L.ec_i8_product_parts_bytes
+    for rows, cols, depth in ((16, 64, 16384), (257, 64, 16384), (0, 64, 16384), (17, 0, 16384), (17, 64, 0), (17, 64, 16400), (17, 64, 131072),
+                              (17, 1 << 31, 16384), (17, (1 << 64) - 1, 16384), ((1 << 64) - 1, 64, 16384), (17, 64, 4992), (17, 64, (1 << 64) - 128)):
+        assert size(rows, cols, depth) == 0, (rows, cols, depth)
+    assert L.ec_i8_linear_workspace_bytes(100, 16384, 0, 0) == 100 * (16384 + 4)
+    for rows in (17, 64, 65, 256):
+        for cols in (1, 64, 1000, 4096):
+            for depth in (5632, 16384, 130944):
+                need, row = size(rows, cols, depth), rows * ((cols + 63) // 64 * 64) * 4
+                if rows <= 64 or cols <= 1000:
+                    assert need >= 2 * row, (rows, cols, depth)
+                # no part is empty, and no more workgroups than fill the units twice
+                parts = need // row
+                assert need == parts * row and parts <= depth // 128 // 8
+                assert parts * -(-rows // 64) * -(-cols // 64) <= 512
+                each = -(-depth // 128 // parts) if parts else 0
+                assert parts * each < depth // 128 + each if parts else True
+    need = size(100, 64, 16384)
+    good = [F, F, 100, F, F, 64, 16384, F, BF16]
+    assert p(None, None, 0, None, None, 8, 128, None, BF16, None, 0, None) == OK
+    assert p(*good, F, need - 1, None) == CAPACITY
+    assert p(*good, F + 8, need, None) == INVALID
+    assert p(*good, None, need, None) == INVALID
+    assert p(F, F, 100, F, F, 8, 100, F, BF16, F, need, None) == INVALID
+    assert p(F, F, 1, F, F, 8, 131072, F, BF16, F, need, None) == UNSUPPORTED
+
+
 def test_linear(L):
     lin = L.ec_i8_linear
     assert L.ec_i8_linear_workspace_bytes(0, 64, 8, 0) == 0
