@@ -575,10 +575,16 @@ uint64_t rows_first(uint64_t rows, uint64_t cols, uint64_t depth, size_t bytes) 
 //   32 x 5120 x 2048: 12.6, 8.5; 4096 x 4096 (24 saved): 12.0, 10.1, but 11.7, 15.2 eager
 //   128 x 4096 x 4096 (16 saved): 12.9, 13.7; twice full, 128 x 8192 x 8192: 24.5, 30.3;
 //   4 stages at least, 32 x 4096 x 4096: 12.3
+// Up to 16 rows, the kernel for them is as fast up to a contraction of 12288:
+//   1 x 8192 x 8192: 16.0 there, 17.2 in parts; 16 x 8192 x 4096: 12.4, 13.0; 1 x 10240 x
+//   4096: 13.5, 13.7; 1 x 12288 x 2048: 13.6, 11.9; 16: 16.0, 12.5; 1 x 16384 x 4096: 21.1,
+//   17.8; 16: 23.2, 18.4; 1 x 16384 x 8192: 33.4, 35.1; 16: 39.7, 36.5; 1 x 32768 x 2048:
+//   35.2, 20.1
 uint32_t parts_of(uint64_t rows, uint64_t cols, uint64_t depth) {
-  if (rows <= kFewRows || rows > EC_I8_MOST_PARTS_ROWS || cols == 0 || cols > EC_MX_MAX_ROWS)
+  if (rows == 0 || rows > EC_I8_MOST_PARTS_ROWS || cols == 0 || cols > EC_MX_MAX_ROWS)
     return 1;
   const uint64_t tiles = ceil_div(rows, 64) * ceil_div(cols, 64), stages = depth / 128;
+  if (rows <= kFewRows && stages < 96) return 1;
   uint64_t most = (rows <= 64 ? 512 : 256) / tiles;
   if (most > stages / 8) most = stages / 8;
   if (most < 2) return 1;

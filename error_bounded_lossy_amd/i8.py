@@ -139,7 +139,7 @@ def i8_product(a: I8Tensor, b: I8Tensor, dtype: torch.dtype = torch.bfloat16,
         _refuse("i8_product: [rows, depth] and [cols, depth] on one GPU are wanted")
     rows, cols = a.lead[0], b.lead[0]
     y = a.home.new_empty((rows, cols), dtype=dtype)
-    need = _b.lib().ec_i8_product_parts_bytes(rows, cols, a.padded) if 16 < rows <= MOST_PARTS_ROWS else 0
+    need = _b.lib().ec_i8_product_parts_bytes(rows, cols, a.padded) if rows <= MOST_PARTS_ROWS else 0
     if need:
         # held until the call is back: before, its kernels are not all enqueued
         ws = a.home.new_empty(need, dtype=torch.int8)

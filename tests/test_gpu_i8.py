@@ -131,7 +131,7 @@ def test_rows_past_whole_tiles(rows, dtype):  # some in a launch of their own
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
-@pytest.mark.parametrize("rows,depth,cols", [(17, 5120, 1), (33, 20000, 40), (64, 6000, 130), (64, 8192, 8100), (65, 8100, 1000),
+@pytest.mark.parametrize("rows,depth,cols", [(1, 12200, 5), (1, 40000, 2000), (16, 16384, 4100), (17, 5120, 1), (33, 20000, 40), (64, 6000, 130), (64, 8192, 8100), (65, 8100, 1000),
                                              (200, 9000, 501), (256, 16384, 250), (256, 5249, 66)])
 def test_product_in_parts_of_the_contraction(rows, depth, cols, dtype):
     a, b = codes(rows, rows, depth), codes(cols + 7, cols, depth)

@@ -50,10 +50,11 @@ def test_products(L):
 
 def test_products_in_parts(L):
     p, size = L.ec_i8_product_parts, L.ec_i8_product_parts_bytes
-    for rows, cols, depth in ((16, 64, 16384), (257, 64, 16384), (0, 64, 16384), (17, 0, 16384), (17, 64, 0), (17, 64, 16400), (17, 64, 131072),
+    for rows, cols, depth in ((16, 64, 12160), (257, 64, 16384), (0, 64, 16384), (17, 0, 16384), (17, 64, 0), (17, 64, 16400), (17, 64, 131072),
                               (17, 1 << 31, 16384), (17, (1 << 64) - 1, 16384), ((1 << 64) - 1, 64, 16384), (17, 64, 4992), (17, 64, (1 << 64) - 128)):
         assert size(rows, cols, depth) == 0, (rows, cols, depth)
     assert L.ec_i8_linear_workspace_bytes(100, 16384, 0, 0) == 100 * (16384 + 4)
+    assert size(1, 128, 12288) == 12 * 128 * 4 and size(16, 8192, 12288) == 4 * 16 * 8192 * 4
     for rows in (17, 64, 65, 256):
         for cols in (1, 64, 1000, 4096):
             for depth in (5632, 16384, 130944):
