@@ -116,6 +116,8 @@ __device__ __forceinline__ void multiply(const i32x4 (&a)[M], const i32x4 (&b)[N
   __builtin_amdgcn_sched_barrier(0);
 }
 
+__host__ __device__ uint32_t part_pitch(uint32_t cols) { return (cols + 63) / 64 * 64; }
+
 // With T = int32_t, a workgroup takes one of p.parts parts of the contraction, and y
 // [parts][rows][part_pitch(cols)] holds the parts' sums, which i8_join adds: the same
 // whole numbers in any order.
@@ -123,9 +125,8 @@ __device__ __forceinline__ void multiply(const i32x4 (&a)[M], const i32x4 (&b)[N
 // STAGES: 2 of the largest tile (of one line each they fill LDS) and where two
 // workgroups share a unit; 4 where there is a unit for each (512 x 8192 x 8192 as tiles
 // of 128 41 us, with 2 stages 45; 2048 x 4096 x 4096 45 and 36), or the tile is small (8
-// stages of tiles of 64, 77 x 2500 x 1111: 5.9 us, 4: 5.2).
-__host__ __device__ uint32_t part_pitch(uint32_t cols) { return (cols + 63) / 64 * 64; }
-
+// stages of tiles of 64, 17 x 1000 x 300: 4.2 us, 4: 3.7; 64 x 16384 x 4096 39.1 and
+// 39.9).
 template <int FM, int FN, int STAGES, typename T, int MODE, bool PAST>
 __global__ __launch_bounds__(256, STAGES * FM * FN >= 16 ? 1 : 2) void i8_tiles(const Product p) {
   constexpr int BM = 64 * FM, BN = 64 * FN, kWaves = 4;
