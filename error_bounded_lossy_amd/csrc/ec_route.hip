@@ -187,9 +187,10 @@ constexpr float kSigmoidOff = 1e-6f, kSoftmaxOff = 1.3e-5f;
 // Whether b, which comes after a, may belong before it: the bias' addition and the
 // places in the lowest bits (`keys` units of each) are relative.  NaN and
 // infinities may.
+constexpr float kBiasOff = 1e-6f;
 __device__ __forceinline__ bool near(float a, float b, float off, int keys) {
   const float size = __builtin_fmaxf(__builtin_fabsf(a), __builtin_fabsf(b));
-  return !(a - b > off + (1e-6f + (float)keys * 0x1p-22f) * size);
+  return !(a - b > off + (kBiasOff + (float)keys * 0x1p-22f) * size);
 }
 
 // Two best keys of a run of 2^shift lanes, from each lane's.
@@ -211,7 +212,8 @@ __device__ __forceinline__ void best_two(K& one, K& two, uint32_t shift) {
 
 // Whether the lane's group is one that is chosen, by each group's two best, whose
 // scores are value(key) (a NaN counts as infinity).  `unsure`: one that is and one
-// that is not are too near.
+// that is not are nearer than what their sums are off by, which goes by the two
+// best's sizes: with biases of both signs the sum may be far smaller.
 template <bool WAVE, typename V, typename KEY, int KEYS, typename F>
 __device__ __forceinline__ bool in_chosen_group(const Layout& s, const Here& a, uint32_t shift,
                                                 const KEY (&key)[KEYS], float off, F&& value,
@@ -229,7 +231,7 @@ __device__ __forceinline__ bool in_chosen_group(const Layout& s, const Here& a, 
     return v != v ? (V)INFINITY : v;
   };
   const V first = is_open(one) ? score_of(one) : (V)-INFINITY;
-  const V score = first + (is_open(two) ? score_of(two) : (V)0);
+  const V second = is_open(two) ? score_of(two) : (V)0, score = first + second;
   uint32_t before = 0;  // groups that come before this one
   for (uint32_t g = 0; g < s.groups; g++) {
     V other;
@@ -241,9 +243,13 @@ __device__ __forceinline__ bool in_chosen_group(const Layout& s, const Here& a, 
   }
   const bool kept = before < s.top_groups;
   if constexpr (sizeof(V) == 4) {
-    const float least = -max_of(kept && a.group < s.groups ? -score : -INFINITY, shift);
-    const float most = max_of(kept || a.group >= s.groups ? -INFINITY : score, shift);
-    unsure |= most > -INFINITY && near(least, most, 2 * off, 0);
+    // (where a sum is infinite, also one too large for 32 bits, there is nothing to compare)
+    const float by = off + 0.5f * kBiasOff * (__builtin_fabsf(first) + __builtin_fabsf(second));
+    const bool any = is_open(one);
+    const float least = -max_of(any && kept ? by - score : -INFINITY, shift);
+    const float most = max_of(any && !kept ? score + by : -INFINITY, shift);
+    unsure |= any && !(by < INFINITY);
+    unsure |= most > -INFINITY && !(least > most);
   }
   return kept;
 }
