@@ -602,17 +602,40 @@ __global__ __launch_bounds__(kThreads) void expert_softmax_back(
   softmax_of(l, shift, top, total, e);
   const Choice m = choice_at(s, row, ids, dweights, token, a.lane);
   const Chosen c = chosen_of(s, shift, m.id >= 0, m.logit, top, total);
-  const double part = m.id >= 0 ? c.weight * ((double)s.scale * (double)m.dw) : 0.0;
-  const double mean = sum_of(part, shift) / total;
+  // p (ds - sum of p ds), with the scores p and their gradients ds, is the sum of
+  // p p_k (ds - ds_k) over all experts: so it keeps its digits where a score is nearly
+  // 1.  What an expert gets that is chosen more than once is added up, in each of its
+  // choices, and its score counts in the first.
+  double d = 0;
+  bool again = false;
+  uint32_t taken = 0;  // of the lane's experts, as bits
+  for (uint32_t j = 0; j < s.choices; j++) {
+    const int32_t id = __shfl(m.id, (int)j, (int)a.lanes);
+    const double v = (double)__shfl(m.dw, (int)j, (int)a.lanes);
+    if (id >= 0 && id == m.id) d += v, again |= j < a.lane;
+    const uint32_t at = (uint32_t)id - expert_at(s, a, 0);
+    if (id >= 0 && at < KEYS) taken |= 1u << at;
+  }
+  d *= (double)s.scale;
+  const bool counts = m.id >= 0 && !again;
+  const double p = counts ? c.weight : 0.0, mine = counts ? d : 0.0;
+  const double mean = sum_of(p * mine, shift) / total;
+  double others = 0;  // the scores' sum without the chosen ones
+#pragma unroll
+  for (int i = 0; i < KEYS; i++) others += taken >> i & 1 ? 0.0 : e[i];
+  double g = d * (sum_of(others, shift) / total);
+  for (uint32_t j = 0; j < s.choices; j++)
+    g += __shfl(p, (int)j, (int)a.lanes) * (d - __shfl(mine, (int)j, (int)a.lanes));
+  g *= c.weight;
   float out[KEYS];
 #pragma unroll
   for (int i = 0; i < KEYS; i++) out[i] = (float)(-e[i] * mean);
   for (uint32_t j = 0; j < s.choices; j++) {
     const int32_t id = __shfl(m.id, (int)j, (int)a.lanes);
-    const float v = __shfl((float)part, (int)j, (int)a.lanes);
+    const float v = __shfl((float)g, (int)j, (int)a.lanes);
     const uint32_t at = (uint32_t)id - expert_at(s, a, 0);
 #pragma unroll
-    for (int i = 0; i < KEYS; i++) out[i] += id >= 0 && at == (uint32_t)i ? v : 0.0f;
+    for (int i = 0; i < KEYS; i++) out[i] = id >= 0 && at == (uint32_t)i ? v : out[i];
   }
   if (a.valid)
     store_logits(dlogits + token * s.experts + expert_at(s, a, 0),
