@@ -556,8 +556,15 @@ __global__ __launch_bounds__(kThreads) void expert_route_back(const float* __res
   const bool here = m.id >= 0;
   const Chosen c = chosen_of(s, s.shift, here, m.logit, 0, 1);
   const double d = here ? (double)s.scale * (double)m.dw : 0.0;
-  const double mean = s.renormalize ? sum_of(here ? d * c.weight : 0.0, s.shift) : 0.0;
-  const float g = here ? (float)(c.weight * (d - mean) * c.opposite) : 0.0f;
+  // Of renormalised weights w, whose sum is 1, d - sum of w d is the sum of w_j (d - d_j):
+  // so it keeps its digits where a weight is nearly 1.
+  double from = d;
+  if (s.renormalize) {
+    from = 0;
+    for (uint32_t j = 0; j < s.choices; j++)
+      from += __shfl(c.weight, (int)j, (int)a.lanes) * (d - __shfl(d, (int)j, (int)a.lanes));
+  }
+  const float g = here ? (float)(c.weight * from * c.opposite) : 0.0f;
   // an expert chosen twice gets both parts, in the choices' order, from each
   float all = 0;
   for (uint32_t j = 0; j < s.choices; j++) {
