@@ -564,13 +564,13 @@ __global__ __launch_bounds__(kThreads) void expert_route_back(const float* __res
     for (uint32_t j = 0; j < s.choices; j++)
       from += __shfl(c.weight, (int)j, (int)a.lanes) * (d - __shfl(d, (int)j, (int)a.lanes));
   }
-  const float g = here ? (float)(c.weight * from * c.opposite) : 0.0f;
+  const double g = here ? c.weight * from * c.opposite : 0.0;
   // an expert chosen twice gets both parts, in the choices' order, from each
-  float all = 0;
+  double all = 0;
   for (uint32_t j = 0; j < s.choices; j++) {
     const int32_t id = __shfl(m.id, (int)j, (int)a.lanes);
-    const float v = __shfl(g, (int)j, (int)a.lanes);
-    all += id == m.id ? v : 0.0f;
+    const double v = __shfl(g, (int)j, (int)a.lanes);
+    all += id == m.id ? v : 0.0;
   }
   const uint64_t first = a.token - (lane >> s.shift);
   auto together = [] {
@@ -580,7 +580,7 @@ __global__ __launch_bounds__(kThreads) void expert_route_back(const float* __res
   for (uint32_t t = 0; t < 64u >> s.shift; t++) {
     if (first + t >= s.tokens) return;
     const bool now = here && lane >> s.shift == t;
-    if (now) mine[m.id] = all;
+    if (now) mine[m.id] = (float)all;
     together();
     T* to = dlogits + (first + t) * s.experts;
     for (uint32_t e0 = lane * E; e0 < s.experts; e0 += 64 * E) {

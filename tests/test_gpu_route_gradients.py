@@ -41,7 +41,7 @@ def exact_gradient(logits, ids, dweights, score, renormalize, scale):
             [a * sum(c * abs(b - x) for c, x in zip(s, ds)) for a, b in zip(s, ds)])
 
 
-MODES = [("softmax", False), ("softmax", True), ("sigmoid", True)]  # and whether weights are renormalised
+MODES = [("softmax", False), ("softmax", True), ("sigmoid", True), ("sigmoid", False)]  # and whether weights are renormalised
 GAPS = [0.0, 4.0, 10.0, 14.0, 17.0, 20.0, 25.0, 30.0, 40.0, 60.0, 85.0]
 
 
@@ -74,7 +74,7 @@ def test_gradients_of_rows_that_are_nearly_certain(experts, choices, renormalize
     check_gradient(l, ids, torch.full((len(GAPS), choices), 0.7), score, renormalize)
 
 
-@pytest.mark.parametrize("score,renormalize", MODES[:1])
+@pytest.mark.parametrize("score,renormalize", MODES)
 @pytest.mark.parametrize("experts", [6, 200])
 def test_gradients_of_an_expert_chosen_twice(experts, renormalize, score):
     g = torch.Generator().manual_seed(experts)
