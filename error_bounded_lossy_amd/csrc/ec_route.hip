@@ -83,8 +83,10 @@ __device__ __forceinline__ double quotient_of(double a, double b) {
 __device__ __forceinline__ double power_of(double x) {  // e^x, x finite and not over 700
   x = x < -1000.0 ? -1000.0 : x;
   const double n = __builtin_rint(x * 1.4426950408889634);
-  double r = __builtin_fma(n, -6.93147180369123816490e-01, x);
-  r = __builtin_fma(n, -1.90821492927058770002e-10, r);
+  // ln 2 in two parts (Cody and Waite): its nearest multiple of 2^-40, whose product
+  // with n is exact, and what is left of it
+  double r = __builtin_fma(n, -0x1.62e42fefa4p-1, x);
+  r = __builtin_fma(n, 0x1.8432a1b0e2634p-43, r);
   double p = 1.0 / 39916800;
   p = __builtin_fma(p, r, 1.0 / 3628800);
   p = __builtin_fma(p, r, 1.0 / 362880);
