@@ -24,8 +24,9 @@ class I8Tensor:
 
     # What the library makes holds both in one allocation, `home`, codes first (`_scales` is None,
     # and `_split` the bytes of codes), and has them as tensors only when asked, as an MXTensor
-    # does.  Addresses are taken at each call.
-    __slots__ = ("cols", "padded", "lead", "home", "_scales", "_split")
+    # does.  Addresses are taken from the tensors at each call: a caller may replace their memory, as
+    # a module does that moves or converts what it holds, but not their form.
+    __slots__ = ("cols", "padded", "lead", "home", "_scales", "_split", "_checked")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
         p = (cols + 127) // 128 * 128
@@ -38,20 +39,41 @@ class I8Tensor:
                     "on one device, are wanted")
         self.cols, self.padded, self.lead = cols, p, form[:-1]
         self.home, self._scales, self._split = codes, scales, codes.numel()
+        self._checked = codes.data_ptr(), scales.data_ptr()
 
     def __reduce__(self):
         return _restored, (self.home, self._scales, tuple(self.lead), self.cols)
 
-    def pointers(self) -> tuple[int, int]:
-        """Where codes and scales are now (a caller may replace their memory, not their form)."""
-        home, scales = self.home, self._scales
+    def _moved(self) -> tuple[int, int]:
+        """The addresses of memory that is not where or what it was: of the same form, or refused."""
+        codes, scales = self.home, self._scales
         if scales is None:
-            start = home.data_ptr()
-            return start, start + self._split
-        if (home.numel() != self._split or scales.numel() * self.padded != self._split
-                or not home.is_contiguous() or not scales.is_contiguous()):
+            ok = codes.shape == (math.prod(self.lead) * (self.padded + 4),)
+        else:
+            ok = (codes.shape == (*self.lead, self.padded) and scales.shape == self.lead
+                  and scales.dtype == torch.float32 and scales.is_contiguous()
+                  and scales.device == codes.device)
+        if not ok or codes.dtype != torch.int8 or not codes.is_contiguous():
             _refuse("I8Tensor: its memory was replaced by some of another form")
-        return home.data_ptr(), scales.data_ptr()
+        start = codes.data_ptr()
+        self._checked = start, start + self._split if scales is None else scales.data_ptr()
+        return self._checked
+
+    def pointers(self) -> tuple[int, int]:
+        """Where codes and scales are now."""
+        home, scales, split = self.home, self._scales, self._split
+        start = home.data_ptr()
+        if scales is None:
+            at = start, start + split
+            return at if at == self._checked else self._moved()
+        at = start, scales.data_ptr()
+        # (the type is looked at each time: a module that is converted twice may have scales of
+        # another one where the first ones were)
+        if (at != self._checked or home.numel() != split or scales.dtype != torch.float32
+                or scales.numel() * self.padded != split or not home.is_contiguous()
+                or not scales.is_contiguous()):
+            return self._moved()
+        return at
 
     @property
     def codes(self) -> torch.Tensor:
@@ -84,6 +106,8 @@ def _empty_i8(lead, cols, like) -> I8Tensor:
     rows = math.prod(lead)
     q._split = rows * q.padded  # a multiple of 128: the scales behind are aligned
     q.home = like.new_empty(q._split + rows * 4, dtype=torch.int8)
+    start = q.home.data_ptr()
+    q._checked = start, start + q._split
     return q
 
 
@@ -97,7 +121,7 @@ def _restored(home, scales, lead, cols) -> I8Tensor:
         _refuse("I8Tensor: int8 memory of codes and scales in one piece is wanted")
     q = object.__new__(I8Tensor)
     q.cols, q.padded, q.lead, q.home = cols, padded, torch.Size(lead), home
-    q._scales, q._split = None, rows * padded
+    q._scales, q._split, q._checked = None, rows * padded, None
     return q
 
 
