@@ -99,11 +99,13 @@ def expert_route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: tor
                             (dweights, logits, ids, score, renormalize, scale), stream)
     r, stride, kind = _logits(logits, score, scale, "expert_route_backward")
     tokens, experts = r.shape
-    if (ids.dim() != 2 or not _ints(ids, (tokens, ids.shape[1])) or ids.shape[1] == 0
+    if (ids.dim() != 2 or ids.dtype != torch.int32 or ids.shape[0] != tokens or ids.shape[1] == 0
             or dweights.dtype != torch.float32 or dweights.shape != ids.shape
             or ids.device != r.device or dweights.device != r.device):
         _refuse("expert_route_backward: int32 ids and float32 dweights [tokens, choices] on the "
                 "logits' device are wanted")
+    if not ids.is_contiguous():
+        ids = ids.contiguous()
     if not dweights.is_contiguous():
         dweights = dweights.contiguous()
     dlogits = r.new_empty((tokens, experts))
