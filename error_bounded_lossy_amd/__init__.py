@@ -145,6 +145,7 @@ def lib():
         ("ec_i8_product_parts", st, (vp, vp, u64, vp, vp, u64, u64, vp, i, vp, sz, vp)),
         ("ec_i8_product_experts", st, (vp, vp, u64, vp, vp, u64, u64, vp, u32, vp, i, vp)),
         ("ec_i8_product_tile", u32, (u64, u64, u64, i, u32)),
+        ("ec_i8_product_rows_first", u64, (u64, u64, u64, i)),
         ("ec_i8_linear_workspace_bytes", sz, (u64, u64, u64, u32)),
         ("ec_i8_linear", st, (vp, i, u64, u64, u64, vp, vp, u64, vp, u32, vp, vp, sz, vp)),
         ("ec_rms_norm", st, (vp, u64, vp, u64, i, u64, u64, vp, i, f32, vp, vp, vp, vp)),

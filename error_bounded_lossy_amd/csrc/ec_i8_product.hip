@@ -682,12 +682,21 @@ ec_status product(Product p, int type, void* workspace, hipStream_t s) {
   }
 }
 
+// Sizes and type that a product takes.
+ec_status check_sizes(uint64_t rows, uint64_t cols, uint64_t depth, int type) {
+  if (!type_known(type) || cols == 0 || depth == 0 || depth % 128 != 0) return EC_ERR_INVALID;
+  return rows > EC_MX_MAX_ROWS || cols > EC_MX_MAX_ROWS || depth > EC_I8_MAX_DEPTH
+             ? EC_ERR_UNSUPPORTED
+             : EC_OK;
+}
+bool is_product(uint64_t rows, uint64_t cols, uint64_t depth, int type) {
+  return check_sizes(rows, cols, depth, type) == EC_OK;
+}
+
 ec_status check(const void* a, const void* sa, uint64_t rows, const void* b, const void* sb,
                 uint64_t cols, uint64_t depth, const void* y, int type) {
-  if (!type_known(type) || cols == 0 || depth == 0 || depth % 128 != 0) return EC_ERR_INVALID;
-  if (rows > EC_MX_MAX_ROWS || cols > EC_MX_MAX_ROWS || depth > EC_I8_MAX_DEPTH)
-    return EC_ERR_UNSUPPORTED;
-  if (rows == 0) return EC_OK;
+  const ec_status st = check_sizes(rows, cols, depth, type);
+  if (st != EC_OK || rows == 0) return st;
   if (!y || !aligned(y, type_bytes(type)) || !read_ok(b, sb) || !read_ok(a, sa))
     return EC_ERR_INVALID;
   return EC_OK;
@@ -761,10 +770,14 @@ ec_status ec_i8_product_experts(const void* a_codes, const void* a_scales, uint6
 
 uint32_t ec_i8_product_tile(uint64_t rows, uint64_t cols, uint64_t depth, int type,
                             uint32_t experts) {
-  if (!type_known(type) || rows == 0 || cols == 0 || depth == 0) return 0;
+  if (rows == 0 || !is_product(rows, cols, depth, type) || experts > EC_MX_MAX_GROUPS) return 0;
   if (few_rows(rows, experts)) return kFewRows;
   return side_of(tiles_for(experts ? kExperts : kDense, rows, cols, depth, experts,
                            type_bytes(type)));
+}
+
+uint64_t ec_i8_product_rows_first(uint64_t rows, uint64_t cols, uint64_t depth, int type) {
+  return is_product(rows, cols, depth, type) ? rows_first(rows, cols, depth, type_bytes(type)) : 0;
 }
 
 size_t ec_i8_linear_workspace_bytes(uint64_t rows, uint64_t depth, uint64_t cols,

@@ -70,10 +70,16 @@ ec_status ec_i8_product_experts(const void* a_codes, const void* a_scales, uint6
                                 uint64_t depth, const int32_t* offsets, uint32_t experts, void* y,
                                 int type, void* stream);
 
-/* Rows and columns of a tile of such a product (experts = 0: ec_i8_product):
- * 256, 128 or 64; 16 where the kernel for few rows runs; 0: no such product. */
+/* What a product of these sizes runs as, where it is taken in one part.
+ * ec_i8_product_tile: rows and columns of a tile (256, 128 or 64; 16 where the
+ * kernel for few rows runs) in ec_i8_product (experts = 0) or
+ * ec_i8_product_experts; 0 if there is no such product.
+ * ec_i8_product_rows_first: the rows that ec_i8_product puts into a launch of
+ * their own, as tiles of 256, before one for the rest (0: all go in one); each
+ * launch's tile is that of its rows. */
 uint32_t ec_i8_product_tile(uint64_t rows, uint64_t cols, uint64_t depth, int type,
                             uint32_t experts);
+uint64_t ec_i8_product_rows_first(uint64_t rows, uint64_t cols, uint64_t depth, int type);
 
 /* y [rows][cols] = Q(x) w^T: x [rows][depth] is quantized along its rows on
  * the way, w [cols][padded(depth)] is in the 8-bit form.  With experts > 0,
