@@ -43,8 +43,10 @@ ec_status ec_rms_norm_i8(const void* x, uint64_t stride, const void* residual,
  *   dx = rstd (weight dy - n mean over the row of weight dy n) + dh, n = h rstd
  *   dweight = sum over the rows of dy n
  * dx is the gradient of x and of the residual alike.  dweight is summed in an
- * order that the sizes fix, its parts in 64 bits; with rows = 0 it is zeros.  The workspace (16-byte
- * aligned) holds ec_rms_norm_backward_workspace_bytes(rows, cols) bytes. */
+ * order that the sizes fix: in fp32 over runs of up to 256 rows and over what
+ * these give to a part, and the parts in 64 bits; with rows = 0 it is zeros.
+ * The workspace (16-byte aligned) holds
+ * ec_rms_norm_backward_workspace_bytes(rows, cols) bytes. */
 size_t ec_rms_norm_backward_workspace_bytes(uint64_t rows, uint64_t cols);
 ec_status ec_rms_norm_backward(const void* dy, const void* h, const void* dh, int type,
                                uint64_t rows, uint64_t cols, const float* rstd, const void* weight,

@@ -2,7 +2,7 @@
 
 Tolerances: h rstd and its product with dy are two roundings, and rstd is off by half of what a sum of a row
 is (64 terms one after the other in a lane, whose sums are joined in 8 steps) and 4 more.  A lane adds what
-its rows give one after the other (here up to 64); the parts are joined in 64 bits."""
+256 rows give one after the other, then such sums; the parts are joined in 64 bits."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -33,10 +33,20 @@ def test_parts_are_joined_in_64_bits():
     assert ((got - want).abs() <= size * U * (FACTORS + 1)).all()
 
 
-@pytest.mark.parametrize("rows,cols", [(1, 64), (65, 1111), (5000, 200), (1001, 1111), (16384, 1024), (300, 20000)])
+# The same in a lane: a large term first, then 2^-25 from up to 2047 rows, of which 255 are lost and not all. Whole runs,
+# one row more, and none behind the first.
+@pytest.mark.parametrize("rows", [1 << 24, (1 << 24) - 5, 256 * 8192, 256 * 8192 + 1, 512 * 8192])
+def test_rows_of_a_lane_are_added_in_runs(rows):
+    dy = torch.full((rows, 8), 2.0 ** -25, device="cuda")
+    dy[:8192] = 1
+    got, want, size = dweight(torch.ones(rows, 8, device="cuda"), dy)
+    assert ((got - want).abs() <= size * U * (FACTORS + 256 + 8 + 1)).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 64), (65, 1111), (5000, 200), (1001, 1111), (16384, 1024), (300, 20000), (70000, 8192), (1 << 22, 65)])
 def test_sums_of_equal_signs(rows, cols):
     g = torch.Generator("cuda").manual_seed(rows)
     x = 0.5 + torch.rand(rows, cols, generator=g, device="cuda")
     got, want, size = dweight(x, torch.rand(rows, cols, generator=g, device="cuda"))
-    # (a row longer than 16384 is summed in two rounds)
-    assert ((got - want).abs() <= size * U * (FACTORS + 32 + 64 + 1)).all()
+    # up to 1024 rows of a lane, in 4 runs; a row longer than 16384 is summed in two rounds
+    assert ((got - want).abs() <= size * U * (FACTORS + 32 + min(rows, 256) + 4 + 1)).all()
