@@ -169,8 +169,9 @@ constexpr uint32_t kRun = 256;
 template <typename T, int PIECES>
 __global__ __launch_bounds__(kMostThreads) void rms_norm_back(const Back p, RowShape s) {
   __shared__ float sums[2][kMostWaves];
-  // (of four pieces the registers hold one row: 2000 x 16384 bf16 72 us, else over 150)
-  constexpr bool kAhead = PIECES <= 3;
+  // (of four pieces, and of three in fp32, the registers hold one row: 2000 x 16384 bf16
+  // 45 us, else 67; 8200 x 5120 fp32 100, else 155)
+  constexpr bool kAhead = PIECES <= (sizeof(T) == 4 ? 2 : 3);
   const uint64_t sets = (s.rows + row_slots(s.shift) - 1) / row_slots(s.shift);
   struct Row {
     Eight<T> dy[PIECES], h[PIECES], dh[PIECES];
