@@ -317,14 +317,17 @@ __global__ __launch_bounds__(kSumCols* kSumSlices) void column_sums(const F from
   double sum = 0;
   if (c < from.cols)
     for (uint64_t r0 = slice; r0 < from.rows; r0 += kSumSlices * kSumAhead) {
+      // (rows past the end read the last one: of a load behind a branch, the conversion
+      // to 64 bits would wait there, 6.4 us)
       float v[kSumAhead];
 #pragma unroll
       for (int i = 0; i < (int)kSumAhead; i++) {
         const uint64_t r = r0 + i * kSumSlices;
-        v[i] = r < from.rows ? from.at(r, (uint32_t)c) : 0.0f;
+        v[i] = from.at(r < from.rows ? r : from.rows - 1, (uint32_t)c);
       }
 #pragma unroll
-      for (int i = 0; i < (int)kSumAhead; i++) sum += v[i];
+      for (int i = 0; i < (int)kSumAhead; i++)
+        sum += r0 + i * kSumSlices < from.rows ? (double)v[i] : 0.0;
     }
   part[slice][col] = sum;
   __syncthreads();
