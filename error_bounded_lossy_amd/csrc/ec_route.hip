@@ -597,12 +597,12 @@ __global__ __launch_bounds__(kThreads) void expert_route_back(const float* __res
 
 // A softmax over all whose weights stay as they are: the gradient reaches every
 // logit.
-template <typename T, int KEYS>
+template <typename T, int KEYS, bool WAVE>
 __global__ __launch_bounds__(kThreads) void expert_softmax_back(
     const float* __restrict__ dweights, const T* __restrict__ logits, Layout s,
     const int32_t* __restrict__ ids, T* dlogits) {
   const Here a = here_of<KEYS>(s);
-  const uint32_t shift = KEYS > 1 ? 6 : s.shift;
+  const uint32_t shift = WAVE ? 6 : s.shift;
   const uint64_t token = a.valid ? a.token : s.tokens - 1;
   const T* row = logits + token * s.stride;
   float l[KEYS];
@@ -611,6 +611,16 @@ __global__ __launch_bounds__(kThreads) void expert_softmax_back(
   softmax_of(l, shift, top, total, e);
   const Choice m = choice_at(s, row, ids, dweights, token, a.lane);
   const Chosen c = chosen_of(s, shift, m.id >= 0, m.logit, top, total);
+  // choice j's value (where it has the whole wave, without the way through LDS)
+  auto of = [&](auto v, uint32_t j) {
+    if constexpr (!WAVE) return __shfl(v, (int)j, (int)a.lanes);
+    else if constexpr (sizeof(v) == 4) return bits_as<decltype(v)>(lane_value(bits_as<uint32_t>(v), (int)j));
+    else {
+      const uint64_t w = bits_as<uint64_t>(v);
+      return bits_as<decltype(v)>((uint64_t)lane_value((uint32_t)(w >> 32), (int)j) << 32 |
+                                  lane_value((uint32_t)w, (int)j));
+    }
+  };
   // p (ds - sum of p ds), with the scores p and their gradients ds, is the sum of
   // p p_k (ds - ds_k) over all experts: so it keeps its digits where a score is nearly
   // 1.  What an expert gets that is chosen more than once is added up, in each of its
@@ -619,8 +629,8 @@ __global__ __launch_bounds__(kThreads) void expert_softmax_back(
   bool again = false;
   uint32_t taken = 0;  // of the lane's experts, as bits
   for (uint32_t j = 0; j < s.choices; j++) {
-    const int32_t id = __shfl(m.id, (int)j, (int)a.lanes);
-    const double v = (double)__shfl(m.dw, (int)j, (int)a.lanes);
+    const int32_t id = of(m.id, j);
+    const double v = (double)of(m.dw, j);
     if (id >= 0 && id == m.id) d += v, again |= j < a.lane;
     const uint32_t at = (uint32_t)id - expert_at(s, a, 0);
     if (id >= 0 && at < KEYS) taken |= 1u << at;
@@ -628,20 +638,20 @@ __global__ __launch_bounds__(kThreads) void expert_softmax_back(
   d *= (double)s.scale;
   const bool counts = m.id >= 0 && !again;
   const double p = counts ? c.weight : 0.0, mine = counts ? d : 0.0;
-  const double mean = sum_of(p * mine, shift) / total;
+  const double part = quotient_of(1.0, total), mean = sum_of(p * mine, shift) * part;
   double others = 0;  // the scores' sum without the chosen ones
 #pragma unroll
   for (int i = 0; i < KEYS; i++) others += taken >> i & 1 ? 0.0 : e[i];
-  double g = d * (sum_of(others, shift) / total);
+  double g = d * (sum_of(others, shift) * part);
   for (uint32_t j = 0; j < s.choices; j++)
-    g += __shfl(p, (int)j, (int)a.lanes) * (d - __shfl(mine, (int)j, (int)a.lanes));
+    g += of(p, j) * (d - of(mine, j));
   g *= c.weight;
   float out[KEYS];
 #pragma unroll
   for (int i = 0; i < KEYS; i++) out[i] = (float)(-e[i] * mean);
   for (uint32_t j = 0; j < s.choices; j++) {
-    const int32_t id = __shfl(m.id, (int)j, (int)a.lanes);
-    const float v = __shfl((float)g, (int)j, (int)a.lanes);
+    const int32_t id = of(m.id, j);
+    const float v = of((float)g, j);
     const uint32_t at = (uint32_t)id - expert_at(s, a, 0);
 #pragma unroll
     for (int i = 0; i < KEYS; i++) out[i] = id >= 0 && at == (uint32_t)i ? v : out[i];
@@ -748,11 +758,14 @@ ec_status back_of(const float* dweights, const void* logits, Layout s, const int
     return launched();
   }
   switch (lay_out(s, 64)) {  // one group: 16 keys at most
-    case 1: go(expert_softmax_back<T, 1>); break;
-    case 2: go(expert_softmax_back<T, 2>); break;
-    case 4: go(expert_softmax_back<T, 4>); break;
-    case 8: go(expert_softmax_back<T, 8>); break;
-    default: go(expert_softmax_back<T, 16>);
+    case 1:
+      if (s.shift == 6) go(expert_softmax_back<T, 1, true>);
+      else go(expert_softmax_back<T, 1, false>);
+      break;
+    case 2: go(expert_softmax_back<T, 2, true>); break;
+    case 4: go(expert_softmax_back<T, 4, true>); break;
+    case 8: go(expert_softmax_back<T, 8, true>); break;
+    default: go(expert_softmax_back<T, 16, true>);
   }
   return launched();
 }
