@@ -46,12 +46,15 @@ GAPS = [0.0, 4.0, 10.0, 14.0, 17.0, 20.0, 25.0, 30.0, 40.0, 60.0, 85.0]
 
 
 def check_gradient(l, ids, dw, score, renormalize, scale=1.0):
+    kind = torch.finfo(l.dtype)
+    step, least = (0.0, 2.0 ** -150) if l.dtype == torch.float32 else (kind.eps / 2, kind.tiny * kind.eps)
     got = ec.expert_route_backward(dw.cuda(), l.cuda(), ids.cuda(), score, renormalize, scale).cpu()
     for t in range(len(l)):
         row = zip(got[t].tolist(), *exact_gradient(l[t].tolist(), ids[t].tolist(), dw[t].tolist(), score, renormalize, scale))
         for e, (d, want, size) in enumerate(row):
-            # 64 bits whose exponentials and quotients are good to some 1e-14, then one rounding to fp32
-            off = float(abs(want)) * U * (1 + 1e-6) + float(size) * 1e-13 + 2.0 ** -150
+            # 64 bits whose exponentials and quotients are good to some 1e-14, one rounding to fp32, and of a
+            # 16-bit type another
+            off = float(abs(want)) * (U + step) * (1 + 1e-6) + float(size) * 1e-13 + least
             assert abs(d - float(want)) <= off, (t, e, d, float(want), off)
 
 
@@ -85,3 +88,22 @@ def test_gradients_of_an_expert_chosen_twice(experts, renormalize, score):
     check_gradient(l, ids, dw, score, renormalize)
     dw[:, 1] = -dw[:, 0] * (1 + 1e-6)  # the two parts nearly cancel
     check_gradient(l, ids, dw, score, renormalize)
+
+
+@pytest.mark.parametrize("score,renormalize", MODES)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["float16", "bfloat16"])
+def test_gradients_in_16_bits(dtype, renormalize, score):
+    g = torch.Generator().manual_seed(7)
+    l = torch.randn(6, 70, generator=g)
+    l[:, 9] += torch.tensor([0.0, 3.0, 8.0, 12.0, 20.0, 60.0])
+    ids = l.sort(dim=1, descending=True).indices[:, :5].int()
+    check_gradient(l.to(dtype), ids, torch.randn(6, 5, generator=g), score, renormalize, 2.5)
+
+
+@pytest.mark.parametrize("score,renormalize", MODES)
+def test_gradients_of_scores_without_digits(renormalize, score):
+    # sigmoids whose sum 64 bits do not hold, beside some that they do, and scores that 32 bits do not
+    l = torch.tensor([[-800.0, -801.0, -820.0, -1e4], [-599.0, -601.0, -700.5, -605.25], [-90.0, -100.0, -104.5, -120.0],
+                      [95.0, 100.0, 104.5, 300.0], [-700.0, 0.5, -1.0, 700.0]])
+    ids = torch.tensor([[0, 1, 2], [0, 1, 3], [1, 0, 2], [3, 2, 1], [1, 2, 0]], dtype=torch.int32)
+    check_gradient(l, ids, torch.randn(5, 3, generator=torch.Generator().manual_seed(8)), score, renormalize, 0.5)
